@@ -235,6 +235,71 @@ AWQ_API awq_status awq_gemm_w4a16(const awq_f16* X, int64_t M, const uint32_t* q
                           int bits, int group, const float* inv_s, unsigned flags, awq_f16* Y,
                           void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- fused epilogue
+ * The W4A16 product with what follows a linear layer in a model, in one call:
+ *     Y[m, n] = act(P[m, n] + bias[n]) * mul[m, n] + residual[m, n],
+ *     P[m, n] = sum_k X[m, k] * inv_s[k] * (q[n, k] - z[k/128, n]) * scale[k/128, n],
+ * in fp32 with one rounding to Y's type at the end. bias [N], mul [M, N] and residual [M, N]
+ * have X's type and may each be NULL (the part is left out). A gated MLP is two calls: up,
+ * then gate with act = AWQ_ACT_SILU and mul = up's output. act, with v = P + bias:
+ *     NONE v; RELU max(v, 0); SILU v / (1 + exp(-v)); GELU v (1 + erf(v / sqrt 2)) / 2;
+ *     GELU_TANH v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2.
+ * mul or residual may be Y itself (each output is read before it is written, by the same
+ * thread); apart from that Y overlaps no input. The other arguments, the flags and the
+ * no-ops are awq_gemm_w4a16's. Activations scaled by inv_s are rounded to 16 bits in the
+ * decode kernel; the tensor-core kernel rounds (q - z) * scale * inv_s[k] once, from fp32.
+ * workspace: at least awq_gemm_epilogue_workspace_size(M, N, K, bits) bytes. */
+#define AWQ_ACT_NONE 0
+#define AWQ_ACT_RELU 1
+#define AWQ_ACT_SILU 2
+#define AWQ_ACT_GELU 3
+#define AWQ_ACT_GELU_TANH 4
+AWQ_API size_t awq_gemm_epilogue_workspace_size(int64_t M, int64_t N, int64_t K, int bits);
+AWQ_API awq_status awq_gemm_w4a16_epilogue(
+    const awq_f16* X, int64_t M, const uint32_t* qweight, const awq_f16* scales,
+    const uint8_t* zeros, int64_t N, int64_t K, int bits, int group, const float* inv_s,
+    const awq_f16* bias, int act, const awq_f16* mul, const awq_f16* residual, unsigned flags,
+    awq_f16* Y, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- expert layers
+ * The operators of a layer whose tokens go to different experts (mixture of experts), for
+ * rows sorted by expert: expert e has the rows offsets[e] .. offsets[e + 1] - 1 of X, any
+ * number of them, none included. offsets: int32 device array [E + 1], nondecreasing, within
+ * 0 .. T (4-byte aligned); it is read on the device only, so a router's output can be passed
+ * without waiting for it. Rows before offsets[0] and from offsets[E] on belong to no expert:
+ * their outputs are left as they were. (Offsets that break the rule give meaningless values in
+ * rows of the output, but nothing outside the arguments' extents is read or written.)
+ * 1 <= E <= 1024. T = 0 is a no-op but for the statistics.
+ *
+ * awq_gemm_w4a16_grouped: awq_gemm_w4a16_epilogue's product, each row against its expert's
+ * packed weight: qweight [E, N, K/8] (or [E, N, 3K/32]), scales [E, K/128, N], zeros
+ * [E, K/128, N], inv_s NULL or [E, K], bias NULL or [E, N]; mul, residual, Y [T, N]. Only the
+ * weights of experts with rows are read. E * N and E * K / 128 must be below 2^31. */
+AWQ_API size_t awq_gemm_grouped_workspace_size(int64_t T, int64_t E, int64_t N, int64_t K, int bits);
+AWQ_API awq_status awq_gemm_w4a16_grouped(
+    const awq_f16* X, int64_t T, const int32_t* offsets, int64_t E, const uint32_t* qweight,
+    const awq_f16* scales, const uint8_t* zeros, int64_t N, int64_t K, int bits, int group,
+    const float* inv_s, const awq_f16* bias, int act, const awq_f16* mul,
+    const awq_f16* residual, unsigned flags, awq_f16* Y, void* workspace, size_t ws_bytes,
+    void* stream);
+
+/* awq_act_stats_grouped: s_x[e, k] = mean over expert e's rows of |X[row, k]| (fp64 sums,
+ * rounded once), 0 for an expert without rows. X: fp16 [T, K], K % 8 == 0; s_x: fp32 [E, K],
+ * every value written, with T = 0 too.
+ * workspace: at least awq_act_stats_grouped_workspace_size(T, E, K) bytes. */
+AWQ_API size_t awq_act_stats_grouped_workspace_size(int64_t T, int64_t E, int64_t K);
+AWQ_API awq_status awq_act_stats_grouped(const awq_f16* X, int64_t T, const int32_t* offsets,
+                                         int64_t E, int64_t K, float* s_x, void* workspace,
+                                         size_t ws_bytes, void* stream);
+
+/* awq_silu_mul_gemm_grouped: awq_silu_mul_gemm with each row against its expert's fp16
+ * weights W_gate, W_up [E, I, K] (the calibration input of the experts' down projections).
+ * H: fp16 [T, I]. E * I must be below 2^31. No workspace. */
+AWQ_API awq_status awq_silu_mul_gemm_grouped(const awq_f16* X, int64_t T, const int32_t* offsets,
+                                             int64_t E, const awq_f16* W_gate,
+                                             const awq_f16* W_up, int64_t I, int64_t K,
+                                             awq_f16* H, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

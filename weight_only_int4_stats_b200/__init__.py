@@ -15,7 +15,8 @@ import torch
 __all__ = [
     "AwqError", "lib", "load_library", "library_path", "GROUP",
     "awq_act_stats", "awq_act_stats_noalloc", "awq_quantize_pack", "awq_search_scale", "awq_gemm_w4a16",
-    "awq_silu_mul_gemm",
+    "awq_silu_mul_gemm", "awq_gemm_w4a16_epilogue", "awq_gemm_w4a16_grouped",
+    "awq_act_stats_grouped", "awq_silu_mul_gemm_grouped", "ACTIVATIONS",
     "awq_check_error", "packed_words_per_row", "WEIGHTS_READY", "BF16",
 ]
 
@@ -65,6 +66,15 @@ def load_library(path: str) -> ctypes.CDLL:
         "awq_silu_mul_gemm": (I32, [P, I64, P, P, I64, I64, P, P]),
         "awq_gemm_w4a16": (I32, [P, I64, P, P, P, I64, I64, I32, I32, P, ctypes.c_uint, P,
                                  P, SZ, P]),
+        "awq_gemm_epilogue_workspace_size": (SZ, [I64, I64, I64, I32]),
+        "awq_gemm_w4a16_epilogue": (I32, [P, I64, P, P, P, I64, I64, I32, I32, P, P, I32, P, P,
+                                          ctypes.c_uint, P, P, SZ, P]),
+        "awq_gemm_grouped_workspace_size": (SZ, [I64, I64, I64, I64, I32]),
+        "awq_gemm_w4a16_grouped": (I32, [P, I64, P, I64, P, P, P, I64, I64, I32, I32, P, P, I32,
+                                         P, P, ctypes.c_uint, P, P, SZ, P]),
+        "awq_act_stats_grouped_workspace_size": (SZ, [I64, I64, I64]),
+        "awq_act_stats_grouped": (I32, [P, I64, P, I64, I64, P, P, SZ, P]),
+        "awq_silu_mul_gemm_grouped": (I32, [P, I64, P, I64, P, P, I64, I64, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -269,4 +279,161 @@ def awq_silu_mul_gemm(X: torch.Tensor, W_gate: torch.Tensor, W_up: torch.Tensor,
     _need(H, torch.float16, "out")
     _check("awq_silu_mul_gemm", lib().awq_silu_mul_gemm(
         _ptr(X), M, _ptr(W_gate), _ptr(W_up), I, K, _ptr(H), _stream(stream)))
+    return H
+
+
+# ------------------------------------------------------------------ fused epilogue, experts
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}   # AWQ_ACT_*
+
+
+def _arg(t, dtype, shape, device, name):
+    """The address of a contiguous CUDA tensor of this dtype, shape and device (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise TypeError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} "
+                        f"on {device}, got {t.dtype} {tuple(t.shape)} on {t.device} "
+                        f"(contiguous={t.is_contiguous()})")
+    return t.data_ptr()
+
+
+def _act(act):
+    try:
+        return ACTIVATIONS[act]
+    except KeyError:
+        raise ValueError(f"act: expected one of {', '.join(ACTIVATIONS)}, got {act!r}") from None
+
+
+def _new(shape, dtype, device, stream):
+    """An output for the call to write: from the allocator's pool of the stream that writes it,
+    so that no earlier use of the memory can still be pending on another one."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _call(fn, device, stream, need, workspace, args):
+    """Calls the C entry point `fn` with `args`, then (workspace, its bytes) unless need is
+    None, then the stream; on the inputs' device, with scratch memory that belongs to the
+    stream that uses it."""
+    if not device.type == "cuda":
+        raise TypeError(f"{fn}: expected CUDA tensors, got {device}")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(fn, device, stream, need, workspace, args)
+    s = torch.cuda.current_stream() if stream is None else stream
+    if need is not None:
+        ws = workspace
+        if ws is None and need > 0:
+            ws = _new(need, torch.uint8, device, stream)
+        if ws is None:
+            args += (None, 0)
+        else:
+            if ws.device != device or not ws.is_contiguous():
+                raise TypeError(f"workspace: expected a contiguous tensor on {device}")
+            args += (ws.data_ptr(), ws.numel() * ws.element_size())
+    _check(fn, getattr(lib(), fn)(*args, s.cuda_stream))
+
+
+def _activations(X, K):
+    if X.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"X: expected torch.float16 or torch.bfloat16, got {X.dtype}")
+    if X.dim() != 2:
+        raise TypeError(f"X: expected a 2-d tensor, got shape {tuple(X.shape)}")
+    return _arg(X, X.dtype, (X.shape[0], K), X.device, "X")
+
+
+def awq_gemm_w4a16_epilogue(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
+                            zeros: torch.Tensor, N: int, K: int, bits: int = 4,
+                            group: int = GROUP, inv_s: torch.Tensor | None = None,
+                            bias: torch.Tensor | None = None, act: str = "none",
+                            mul: torch.Tensor | None = None,
+                            residual: torch.Tensor | None = None,
+                            out: torch.Tensor | None = None, workspace=None, stream=None,
+                            weights_ready: bool = False) -> torch.Tensor:
+    """Y = act(X diag(inv_s) deq(W)^T + bias) * mul + residual ([M, N], X's dtype), in fp32 with
+    one rounding at the end.
+
+    X fp16 or bf16 [M, K]; bias [N], mul and residual [M, N] in X's dtype, each optional; act a
+    key of ACTIVATIONS. ``out`` may be ``mul`` or ``residual`` itself. ``weights_ready`` as for
+    awq_gemm_w4a16."""
+    dev, t = X.device, X.dtype
+    x, M = _activations(X, K), X.shape[0]
+    Y = _new((M, N), t, dev, stream) if out is None else out
+    _call("awq_gemm_w4a16_epilogue", dev, stream,
+          lib().awq_gemm_epilogue_workspace_size(M, N, K, bits), workspace,
+          (x, M, _arg(qweight, torch.int32, (N, packed_words_per_row(K, bits)), dev, "qweight"),
+           _arg(scales, torch.float16, (K // GROUP, N), dev, "scales"),
+           _arg(zeros, torch.uint8, (K // GROUP, N), dev, "zeros"), N, K, bits, group,
+           _arg(inv_s, torch.float32, (K,), dev, "inv_s"), _arg(bias, t, (N,), dev, "bias"),
+           _act(act), _arg(mul, t, (M, N), dev, "mul"),
+           _arg(residual, t, (M, N), dev, "residual"),
+           (WEIGHTS_READY if weights_ready else 0) | (BF16 if t == torch.bfloat16 else 0),
+           _arg(Y, t, (M, N), dev, "out")))
+    return Y
+
+
+def awq_gemm_w4a16_grouped(X: torch.Tensor, offsets: torch.Tensor, qweight: torch.Tensor,
+                           scales: torch.Tensor, zeros: torch.Tensor, N: int, K: int,
+                           bits: int = 4, group: int = GROUP,
+                           inv_s: torch.Tensor | None = None,
+                           bias: torch.Tensor | None = None, act: str = "none",
+                           mul: torch.Tensor | None = None,
+                           residual: torch.Tensor | None = None,
+                           out: torch.Tensor | None = None, workspace=None, stream=None,
+                           weights_ready: bool = False) -> torch.Tensor:
+    """awq_gemm_w4a16_epilogue for rows sorted by expert: expert e's rows of X [T, K] are
+    offsets[e] .. offsets[e + 1] - 1 (int32 [E + 1] on the GPU, read there only).
+
+    qweight [E, N, words], scales and zeros [E, K // 128, N], inv_s [E, K], bias [E, N]; mul,
+    residual and the result [T, N]. Rows of no expert are left as they were in ``out``
+    (undefined without it)."""
+    dev, t = X.device, X.dtype
+    x, T, E = _activations(X, K), X.shape[0], offsets.numel() - 1
+    Y = _new((T, N), t, dev, stream) if out is None else out
+    _call("awq_gemm_w4a16_grouped", dev, stream,
+          lib().awq_gemm_grouped_workspace_size(T, E, N, K, bits), workspace,
+          (x, T, _arg(offsets, torch.int32, (E + 1,), dev, "offsets"), E,
+           _arg(qweight, torch.int32, (E, N, packed_words_per_row(K, bits)), dev, "qweight"),
+           _arg(scales, torch.float16, (E, K // GROUP, N), dev, "scales"),
+           _arg(zeros, torch.uint8, (E, K // GROUP, N), dev, "zeros"), N, K, bits, group,
+           _arg(inv_s, torch.float32, (E, K), dev, "inv_s"),
+           _arg(bias, t, (E, N), dev, "bias"), _act(act), _arg(mul, t, (T, N), dev, "mul"),
+           _arg(residual, t, (T, N), dev, "residual"),
+           (WEIGHTS_READY if weights_ready else 0) | (BF16 if t == torch.bfloat16 else 0),
+           _arg(Y, t, (T, N), dev, "out")))
+    return Y
+
+
+def awq_act_stats_grouped(X: torch.Tensor, offsets: torch.Tensor,
+                          out: torch.Tensor | None = None, workspace=None,
+                          stream=None) -> torch.Tensor:
+    """s_x[e, k] = mean |X[row, k]| over expert e's rows offsets[e] .. offsets[e + 1] - 1 (fp32
+    [E, K]; 0 for an expert without rows), for fp16 X [T, K] sorted by expert and int32 offsets
+    [E + 1] on the GPU."""
+    dev, (T, K), E = X.device, X.shape, offsets.numel() - 1
+    s_x = _new((E, K), torch.float32, dev, stream) if out is None else out
+    _call("awq_act_stats_grouped", dev, stream,
+          lib().awq_act_stats_grouped_workspace_size(T, E, K), workspace,
+          (_arg(X, torch.float16, (T, K), dev, "X"), T,
+           _arg(offsets, torch.int32, (E + 1,), dev, "offsets"), E, K,
+           _arg(s_x, torch.float32, (E, K), dev, "out")))
+    return s_x
+
+
+def awq_silu_mul_gemm_grouped(X: torch.Tensor, offsets: torch.Tensor, W_gate: torch.Tensor,
+                              W_up: torch.Tensor, out: torch.Tensor | None = None,
+                              stream=None) -> torch.Tensor:
+    """H = silu(X W_gate[e]^T) * (X W_up[e]^T) (fp16 [T, I]) for rows sorted by expert: expert
+    e's rows of X [T, K] are offsets[e] .. offsets[e + 1] - 1; W_gate, W_up fp16 [E, I, K]."""
+    dev, (T, K) = X.device, X.shape
+    E, I = offsets.numel() - 1, W_gate.shape[1]
+    H = _new((T, I), torch.float16, dev, stream) if out is None else out
+    f16 = torch.float16
+    _call("awq_silu_mul_gemm_grouped", dev, stream, None, None,
+          (_arg(X, f16, (T, K), dev, "X"), T,
+           _arg(offsets, torch.int32, (E + 1,), dev, "offsets"), E,
+           _arg(W_gate, f16, (E, I, K), dev, "W_gate"), _arg(W_up, f16, (E, I, K), dev, "W_up"),
+           I, K, _arg(H, f16, (T, I), dev, "out")))
     return H

@@ -99,4 +99,99 @@ inline int act_stats_splits(int64_t M, int64_t K, int num_sms) {
   return static_cast<int>(s);
 }
 
+// ---------------------------------------------------------------------------------------
+// The statistic of each expert: s_x[e, k] = mean over e's rows of |x[row, k]|, rows sorted by
+// expert, expert e's from offsets[e] to offsets[e + 1] (0 for an expert without rows).
+//
+// Rows are cut into slices of equal length wherever the experts begin, so the work is balanced
+// whatever the routing, and no launch waits for the offsets on the host. A slice that holds
+// rows of several experts sums each of them apart. The partial sums of slice y and expert e go
+// to slot y + e of the workspace: along the rows either the slice or the expert moves on, so
+// the slots of (slice, expert) pairs that share rows are all different, and there are at most
+// slices + E of them.
+inline int64_t grouped_stats_rows(int64_t T, int64_t K, int num_sms) {
+  const int64_t splits = act_stats_splits(T, K, num_sms);
+  return (T + splits - 1) / splits;
+}
+inline int64_t grouped_stats_slices(int64_t T, int64_t K, int num_sms) {
+  const int64_t rows = grouped_stats_rows(T, K, num_sms);
+  return (T + rows - 1) / rows;
+}
+
+// offsets[e] as a row of X: a value outside 0 .. T is taken as the nearest end.
+__device__ __forceinline__ int64_t row_offset(const int* __restrict__ offsets, int e, int64_t T) {
+  const int64_t v = offsets[e];
+  return v < 0 ? 0 : v > T ? T : v;
+}
+
+__global__ void __launch_bounds__(256) act_stats_grouped_partial_kernel(
+    const __half* __restrict__ X, int64_t T, int64_t K, const int* __restrict__ offsets, int E,
+    int64_t rows, double* __restrict__ part) {
+  const int lane = threadIdx.x & 31;
+  const int rl = threadIdx.x >> 5;
+  const int64_t col0 = static_cast<int64_t>(blockIdx.x) * kStatsCols + lane * 8;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kStatsCols + threadIdx.x;
+  const int64_t y0 = static_cast<int64_t>(blockIdx.y) * rows;
+  const int64_t y1 = min(T, y0 + rows);
+  __shared__ double red[kStatsRowLanes][kStatsCols];
+  // the first expert that ends behind the slice's first row: every one before it ends earlier
+  int e = 0;
+  for (int n = E; n > 0;) {
+    const int half = n >> 1;
+    if (row_offset(offsets, e + half + 1, T) <= y0) {
+      e += half + 1;
+      n -= half + 1;
+    } else {
+      n = half;
+    }
+  }
+  for (; e < E; ++e) {
+    const int64_t a = row_offset(offsets, e, T);
+    if (a >= y1) break;
+    const int64_t r0 = max(a, y0), r1 = min(row_offset(offsets, e + 1, T), y1);
+    if (r0 >= r1) continue;   // no rows of this expert
+    double acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.0;
+    if (col0 < K)
+      for (int64_t r = r0 + rl; r < r1; r += kStatsRowLanes) {
+        const uint4 v = AWQ_IN_BOUNDS(r < T && col0 + 8 <= K) ? ldg_nc_v4(X + r * K + col0)
+                                                              : make_uint4(0u, 0u, 0u, 0u);
+        const __half2* h = reinterpret_cast<const __half2*>(&v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __half22float2(h[i]);
+          acc[2 * i] += fabs(static_cast<double>(f.x));
+          acc[2 * i + 1] += fabs(static_cast<double>(f.y));
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[rl][lane * 8 + i] = acc[i];
+    __syncthreads();
+    if (c < K) {
+      double s = 0.0;
+#pragma unroll
+      for (int j = 0; j < kStatsRowLanes; ++j) s += red[j][threadIdx.x];
+      if (AWQ_IN_BOUNDS(blockIdx.y + static_cast<int64_t>(e) < gridDim.y + static_cast<int64_t>(E)))
+        part[(blockIdx.y + static_cast<int64_t>(e)) * K + c] = s;
+    }
+    __syncthreads();
+  }
+}
+
+__global__ void act_stats_grouped_finish_kernel(const double* __restrict__ part, int64_t T,
+                                                int64_t K, const int* __restrict__ offsets,
+                                                int64_t rows, float* __restrict__ s_x) {
+  const int64_t k = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int e = blockIdx.y;
+  if (k >= K) return;
+  const int64_t a = row_offset(offsets, e, T), b = row_offset(offsets, e + 1, T);
+  double s = 0.0;
+  if (a < b) {
+    for (int64_t y = a / rows; y <= (b - 1) / rows; ++y) s += part[(y + e) * K + k];
+    s /= static_cast<double>(b - a);
+  }
+  s_x[e * K + k] = __double2float_rn(s);
+}
+
 }  // namespace awq

@@ -83,14 +83,14 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, in
   return r == CUDA_SUCCESS;
 }
 
-template <int BN, ASrc kA, Epi kEpi, bool kBf16, int kBlkT>
+template <int BN, ASrc kA, Epi kEpi, bool kBf16, int kBlkT, bool kGrp = false>
 awq_status launch_tc_blk(const void* Xop, int64_t M, const void* Aop, int64_t a_rows,
                          const awq::TcArgs& args, cudaStream_t st, const void* Aop2) {
-  using L = awq::TcLayout<BN, kA, kBlkT>;
+  using L = awq::TcLayout<BN, kA, kBlkT, kGrp>;
   static std::atomic<bool> attr_set[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return AWQ_ERR_CUDA;
-  auto kern = awq::tc_gemm_kernel<BN, kA, kEpi, kBf16, kBlkT>;
+  auto kern = awq::tc_gemm_kernel<BN, kA, kEpi, kBf16, kBlkT, kGrp>;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem) !=
         cudaSuccess)
@@ -131,7 +131,7 @@ awq_status launch_tc_blk(const void* Xop, int64_t M, const void* Aop, int64_t a_
                     awq::kTcBK, true))
     return AWQ_ERR_CUDA;
   if ((kA == ASrc::kPacked4 || kA == ASrc::kPacked3) && args.N % 16 == 0) {
-    const int64_t G = args.K / awq::kGroup;
+    const int64_t G = args.K / awq::kGroup * (kGrp ? args.E : 1);
     if (!make_tmap_2d(&ts, args.scales, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, G, args.N, L::kPG,
                       awq::kTcBM, false) ||
         !make_tmap_2d(&tz, args.zeros, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, G, args.N, L::kPG,
@@ -141,6 +141,10 @@ awq_status launch_tc_blk(const void* Xop, int64_t M, const void* Aop, int64_t a_
   }
   a.m_tiles = static_cast<int>((M + BN - 1) / BN);
   a.row_tiles = static_cast<int>((a_rows + awq::kTcBM - 1) / awq::kTcBM);
+  if (kGrp) {   // the row tiles of one expert, and the most token tiles that E experts can have
+    a.row_tiles = static_cast<int>((args.N + awq::kTcBM - 1) / awq::kTcBM);
+    a.m_tiles = static_cast<int>(M / BN + (M < args.E ? M : args.E));
+  }
   a.rows_total = a_rows;
   if (a.k_splits < 1) a.k_splits = 1;
   const int64_t units = static_cast<int64_t>(a.m_tiles) * a.row_tiles * a.k_splits;
@@ -167,17 +171,30 @@ awq_status launch_tc_blk(const void* Xop, int64_t M, const void* Aop, int64_t a_
 // thread set the pace: token tiles up to 128, and inv_s folded into the weights. Plain
 // BN = 256 keeps four one-block stages (two two-block stages, all that fit, measured slower
 // there: 1294 -> 1172 TFLOP/s on [28672, 8192] at M = 4096).
-template <int BN, ASrc kA, Epi kEpi, bool kBf16 = false>
+template <int BN, ASrc kA, Epi kEpi, bool kBf16 = false, bool kGrp = false>
 awq_status launch_tc(const void* Xop, int64_t M, const void* Aop, int64_t a_rows,
                      const awq::TcArgs& args, cudaStream_t st, const void* Aop2 = nullptr) {
   constexpr bool kPk = kA == ASrc::kPacked4 || kA == ASrc::kPacked3;
   if constexpr (kPk && BN == 256) {
     if (args.inv_s == nullptr)
-      return launch_tc_blk<BN, kA, kEpi, kBf16, 1>(Xop, M, Aop, a_rows, args, st, Aop2);
-    return launch_tc_blk<BN, kA, kEpi, kBf16, 2>(Xop, M, Aop, a_rows, args, st, Aop2);
+      return launch_tc_blk<BN, kA, kEpi, kBf16, 1, kGrp>(Xop, M, Aop, a_rows, args, st, Aop2);
+    return launch_tc_blk<BN, kA, kEpi, kBf16, 2, kGrp>(Xop, M, Aop, a_rows, args, st, Aop2);
   } else {
-    return launch_tc_blk<BN, kA, kEpi, kBf16, kPk ? 2 : 1>(Xop, M, Aop, a_rows, args, st, Aop2);
+    return launch_tc_blk<BN, kA, kEpi, kBf16, kPk ? 2 : 1, kGrp>(Xop, M, Aop, a_rows, args, st,
+                                                                 Aop2);
   }
+}
+
+// Grouped launches: the token tile by the mean rows of an expert. (A tile multiplies only the
+// tokens its expert has, so an expert with fewer rows than the mean wastes no MMA work.)
+template <ASrc kA, Epi kEpi, bool kBf16 = false>
+awq_status launch_tc_grouped(const void* Xop, int64_t T, const void* Aop, int64_t a_rows,
+                             const awq::TcArgs& args, cudaStream_t st, const void* Aop2 = nullptr) {
+  const int64_t mean = (T + args.E - 1) / args.E;
+  if (mean <= 32) return launch_tc<32, kA, kEpi, kBf16, true>(Xop, T, Aop, a_rows, args, st, Aop2);
+  if (mean <= 64) return launch_tc<64, kA, kEpi, kBf16, true>(Xop, T, Aop, a_rows, args, st, Aop2);
+  if (mean <= 128) return launch_tc<128, kA, kEpi, kBf16, true>(Xop, T, Aop, a_rows, args, st, Aop2);
+  return launch_tc<256, kA, kEpi, kBf16, true>(Xop, T, Aop, a_rows, args, st, Aop2);
 }
 
 template <ASrc kA, Epi kEpi, bool kBf16 = false>
@@ -818,6 +835,169 @@ awq_status awq_gemm_w4a16(const awq_f16* X, int64_t M, const uint32_t* qweight,
   else
     awq::splitk_reduce_kernel<false><<<rgrid, 256, 0, st>>>(partial, splits, MN,
                                                             reinterpret_cast<__half*>(Y));
+  return launch_status();
+}
+
+// ------------------------------------------------------------------ fused epilogue, experts
+namespace {
+bool bad_ptr16(const void* p) { return p != nullptr && !aligned16(p); }
+
+// What the products with a fused epilogue share: argument checks past the shapes, and the
+// launch. E experts with N rows each; offsets NULL for one expert with every row of X.
+awq_status fused_gemm(const void* X, int64_t T, const int32_t* offsets, int64_t E,
+                      const uint32_t* qweight, const awq_f16* scales, const uint8_t* zeros,
+                      int64_t N, int64_t K, int bits, int group, const float* inv_s,
+                      const awq_f16* bias, int act, const awq_f16* mul, const awq_f16* residual,
+                      unsigned flags, awq_f16* Y, void* workspace, size_t ws_bytes,
+                      cudaStream_t st) {
+  if (bad_dim(T) || bad_dim(N) || bad_dim(K) || K == 0) return AWQ_ERR_INVALID_ARG;
+  if (group != awq::kGroup || K % awq::kGroup != 0) return AWQ_ERR_INVALID_ARG;
+  if (bits != 4 && bits != 3) return AWQ_ERR_INVALID_ARG;
+  if (act < awq::kActNone || act > awq::kActGeluTanh) return AWQ_ERR_INVALID_ARG;
+  if ((flags & ~static_cast<unsigned>(AWQ_GEMM_WEIGHTS_READY | AWQ_GEMM_BF16)) != 0)
+    return AWQ_ERR_INVALID_ARG;
+  if (T == 0 || N == 0) return AWQ_OK;
+  if (!X || !qweight || !scales || !zeros || !Y) return AWQ_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(qweight) || !aligned16(scales) || !aligned16(zeros) ||
+      !aligned16(Y) || bad_ptr16(inv_s) || bad_ptr16(bias) || bad_ptr16(mul) ||
+      bad_ptr16(residual))
+    return AWQ_ERR_INVALID_ARG;
+  // TMA coordinates (weight rows, scale rows) are 32-bit
+  if (E * N > kMaxDim || E * (K / awq::kGroup) > kMaxDim) return AWQ_ERR_INVALID_ARG;
+  const int splits = offsets == nullptr ? splitk_for(T, N, K) : 1;
+  const size_t part_bytes =
+      splits > 1 ? align256(static_cast<size_t>(splits) * T * N * sizeof(float)) : 0;
+  if (part_bytes > 0 && (!workspace || ws_bytes < part_bytes || !aligned16(workspace)))
+    return AWQ_ERR_WORKSPACE;
+  awq::TcArgs args{};
+  args.M = T;
+  args.N = N;
+  args.N_pad = N;
+  args.K = K;
+  args.scales = reinterpret_cast<const __half*>(scales);
+  args.zeros = zeros;
+  args.Y = Y;
+  args.k_splits = splits;
+  args.partial = splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  args.inv_s = inv_s;
+  args.offsets = offsets;
+  args.E = static_cast<int>(E);
+  args.bias = bias;
+  args.mul = mul;
+  args.residual = residual;
+  args.act = act;
+  const bool bf16 = (flags & AWQ_GEMM_BF16) != 0;
+  awq_status r;
+  if (bf16)
+    r = bits == 3 ? launch_tc_grouped<ASrc::kPacked3, Epi::kFused, true>(X, T, qweight, E * N, args, st)
+                  : launch_tc_grouped<ASrc::kPacked4, Epi::kFused, true>(X, T, qweight, E * N, args, st);
+  else
+    r = bits == 3 ? launch_tc_grouped<ASrc::kPacked3, Epi::kFused>(X, T, qweight, E * N, args, st)
+                  : launch_tc_grouped<ASrc::kPacked4, Epi::kFused>(X, T, qweight, E * N, args, st);
+  if (r != AWQ_OK || splits == 1) return r;
+  const unsigned grid = static_cast<unsigned>((T * N + 255) / 256);
+  if (bf16) awq::splitk_fused_kernel<true><<<grid, 256, 0, st>>>(args);
+  else awq::splitk_fused_kernel<false><<<grid, 256, 0, st>>>(args);
+  return launch_status();
+}
+
+bool bad_groups(int64_t E, const int32_t* offsets) {
+  return E < 1 || E > awq::kMaxExperts || offsets == nullptr ||
+         (reinterpret_cast<uintptr_t>(offsets) & 3u) != 0;
+}
+}  // namespace
+
+size_t awq_gemm_epilogue_workspace_size(int64_t M, int64_t N, int64_t K, int bits) {
+  if (M <= 0 || K <= 0 || N <= 0) return 0;
+  (void)bits;
+  const int splits = splitk_for(M, N, K);
+  return splits > 1 ? align256(static_cast<size_t>(splits) * M * N * sizeof(float)) : 0;
+}
+
+awq_status awq_gemm_w4a16_epilogue(const awq_f16* X, int64_t M, const uint32_t* qweight,
+                                   const awq_f16* scales, const uint8_t* zeros, int64_t N,
+                                   int64_t K, int bits, int group, const float* inv_s,
+                                   const awq_f16* bias, int act, const awq_f16* mul,
+                                   const awq_f16* residual, unsigned flags, awq_f16* Y,
+                                   void* workspace, size_t ws_bytes, void* stream) {
+  return fused_gemm(X, M, nullptr, 1, qweight, scales, zeros, N, K, bits, group, inv_s, bias, act,
+                    mul, residual, flags, Y, workspace, ws_bytes,
+                    static_cast<cudaStream_t>(stream));
+}
+
+size_t awq_gemm_grouped_workspace_size(int64_t T, int64_t E, int64_t N, int64_t K, int bits) {
+  (void)T; (void)E; (void)N; (void)K; (void)bits;
+  return 0;
+}
+
+awq_status awq_gemm_w4a16_grouped(const awq_f16* X, int64_t T, const int32_t* offsets, int64_t E,
+                                  const uint32_t* qweight, const awq_f16* scales,
+                                  const uint8_t* zeros, int64_t N, int64_t K, int bits, int group,
+                                  const float* inv_s, const awq_f16* bias, int act,
+                                  const awq_f16* mul, const awq_f16* residual, unsigned flags,
+                                  awq_f16* Y, void* workspace, size_t ws_bytes, void* stream) {
+  if (bad_groups(E, offsets)) return AWQ_ERR_INVALID_ARG;
+  return fused_gemm(X, T, offsets, E, qweight, scales, zeros, N, K, bits, group, inv_s, bias, act,
+                    mul, residual, flags, Y, workspace, ws_bytes,
+                    static_cast<cudaStream_t>(stream));
+}
+
+awq_status awq_silu_mul_gemm_grouped(const awq_f16* X, int64_t T, const int32_t* offsets,
+                                     int64_t E, const awq_f16* W_gate, const awq_f16* W_up,
+                                     int64_t I, int64_t K, awq_f16* H, void* stream) {
+  if (bad_groups(E, offsets)) return AWQ_ERR_INVALID_ARG;
+  if (bad_dim(T) || bad_dim(I) || bad_dim(K) || K == 0) return AWQ_ERR_INVALID_ARG;
+  if (K % awq::kGroup != 0) return AWQ_ERR_INVALID_ARG;
+  if (T == 0 || I == 0) return AWQ_OK;
+  if (!X || !W_gate || !W_up || !H) return AWQ_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(W_gate) || !aligned16(W_up) || !aligned16(H))
+    return AWQ_ERR_INVALID_ARG;
+  if (E * I > kMaxDim) return AWQ_ERR_INVALID_ARG;
+  awq::TcArgs args{};
+  args.M = T;
+  args.N = I;
+  args.N_pad = I;
+  args.K = K;
+  args.Y = H;
+  args.k_splits = 1;
+  args.offsets = offsets;
+  args.E = static_cast<int>(E);
+  return launch_tc_grouped<ASrc::kPair16, Epi::kSiluMul>(
+      X, T, W_gate, E * I, args, static_cast<cudaStream_t>(stream), W_up);
+}
+
+// ------------------------------------------------------------------ act_stats of each expert
+size_t awq_act_stats_grouped_workspace_size(int64_t T, int64_t E, int64_t K) {
+  if (T <= 0 || E <= 0 || K <= 0) return 0;
+  return static_cast<size_t>(awq::grouped_stats_slices(T, K, num_sms()) + E) *
+         static_cast<size_t>(K) * sizeof(double);
+}
+
+awq_status awq_act_stats_grouped(const awq_f16* X, int64_t T, const int32_t* offsets, int64_t E,
+                                 int64_t K, float* s_x, void* workspace, size_t ws_bytes,
+                                 void* stream) {
+  if (bad_groups(E, offsets)) return AWQ_ERR_INVALID_ARG;
+  if (bad_dim(T) || bad_dim(K)) return AWQ_ERR_INVALID_ARG;
+  if (K == 0) return AWQ_OK;
+  if (K % 8 != 0) return AWQ_ERR_INVALID_ARG;
+  if (!s_x || !aligned16(s_x) || (T > 0 && (!X || !aligned16(X)))) return AWQ_ERR_INVALID_ARG;
+  const size_t need = awq_act_stats_grouped_workspace_size(T, E, K);
+  if (need > 0 && (!workspace || ws_bytes < need || !aligned16(workspace)))
+    return AWQ_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  double* part = static_cast<double*>(workspace);
+  const int64_t rows = T > 0 ? awq::grouped_stats_rows(T, K, num_sms()) : 1;
+  if (T > 0) {
+    const int64_t slices = awq::grouped_stats_slices(T, K, num_sms());
+    dim3 g1(static_cast<unsigned>((K + awq::kStatsCols - 1) / awq::kStatsCols),
+            static_cast<unsigned>(slices));
+    awq::act_stats_grouped_partial_kernel<<<g1, 256, 0, st>>>(
+        reinterpret_cast<const __half*>(X), T, K, offsets, static_cast<int>(E), rows, part);
+    awq_status s = launch_status();
+    if (s != AWQ_OK) return s;
+  }
+  dim3 g2(static_cast<unsigned>((K + 255) / 256), static_cast<unsigned>(E));
+  awq::act_stats_grouped_finish_kernel<<<g2, 256, 0, st>>>(part, T, K, offsets, rows, s_x);
   return launch_status();
 }
 
