@@ -274,7 +274,7 @@ AWQ_API awq_status awq_gemm_w4a16_epilogue(
  * awq_gemm_w4a16_grouped: awq_gemm_w4a16_epilogue's product, each row against its expert's
  * packed weight: qweight [E, N, K/8] (or [E, N, 3K/32]), scales [E, K/128, N], zeros
  * [E, K/128, N], inv_s NULL or [E, K], bias NULL or [E, N]; mul, residual, Y [T, N]. Only the
- * weights of experts with rows are read. E * N and E * K / 128 must be below 2^31. */
+ * weights of experts with rows are read. E * N and E * N * K / 128 must be below 2^31. workspace: at least awq_gemm_grouped_workspace_size(T, E, N, K, bits) bytes. */
 AWQ_API size_t awq_gemm_grouped_workspace_size(int64_t T, int64_t E, int64_t N, int64_t K, int bits);
 AWQ_API awq_status awq_gemm_w4a16_grouped(
     const awq_f16* X, int64_t T, const int32_t* offsets, int64_t E, const uint32_t* qweight,

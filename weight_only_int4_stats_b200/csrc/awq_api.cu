@@ -12,6 +12,8 @@
 #include "common.cuh"
 #include "gemm_tc.cuh"
 #include "gemv.cuh"
+#include "gemm_fused.cuh"
+#include "gemv_fused.cuh"
 #include "quantize.cuh"
 #include "search.cuh"
 
@@ -131,7 +133,7 @@ awq_status launch_tc_blk(const void* Xop, int64_t M, const void* Aop, int64_t a_
                     awq::kTcBK, true))
     return AWQ_ERR_CUDA;
   if ((kA == ASrc::kPacked4 || kA == ASrc::kPacked3) && args.N % 16 == 0) {
-    const int64_t G = args.K / awq::kGroup * (kGrp ? args.E : 1);
+    const int64_t G = args.K / awq::kGroup;
     if (!make_tmap_2d(&ts, args.scales, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, G, args.N, L::kPG,
                       awq::kTcBM, false) ||
         !make_tmap_2d(&tz, args.zeros, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, G, args.N, L::kPG,
@@ -185,18 +187,6 @@ awq_status launch_tc(const void* Xop, int64_t M, const void* Aop, int64_t a_rows
   }
 }
 
-// Grouped launches: the token tile by the mean rows of an expert. (A tile multiplies only the
-// tokens its expert has, so an expert with fewer rows than the mean wastes no MMA work.)
-template <ASrc kA, Epi kEpi, bool kBf16 = false>
-awq_status launch_tc_grouped(const void* Xop, int64_t T, const void* Aop, int64_t a_rows,
-                             const awq::TcArgs& args, cudaStream_t st, const void* Aop2 = nullptr) {
-  const int64_t mean = (T + args.E - 1) / args.E;
-  if (mean <= 32) return launch_tc<32, kA, kEpi, kBf16, true>(Xop, T, Aop, a_rows, args, st, Aop2);
-  if (mean <= 64) return launch_tc<64, kA, kEpi, kBf16, true>(Xop, T, Aop, a_rows, args, st, Aop2);
-  if (mean <= 128) return launch_tc<128, kA, kEpi, kBf16, true>(Xop, T, Aop, a_rows, args, st, Aop2);
-  return launch_tc<256, kA, kEpi, kBf16, true>(Xop, T, Aop, a_rows, args, st, Aop2);
-}
-
 template <ASrc kA, Epi kEpi, bool kBf16 = false>
 awq_status launch_tc_bn(const void* Xop, int64_t M, const void* Aop, int64_t a_rows,
                         const awq::TcArgs& args, cudaStream_t st, const void* Aop2 = nullptr) {
@@ -204,6 +194,19 @@ awq_status launch_tc_bn(const void* Xop, int64_t M, const void* Aop, int64_t a_r
   if (M <= 64) return launch_tc<64, kA, kEpi, kBf16>(Xop, M, Aop, a_rows, args, st, Aop2);
   if (M <= 128) return launch_tc<128, kA, kEpi, kBf16>(Xop, M, Aop, a_rows, args, st, Aop2);
   return launch_tc<256, kA, kEpi, kBf16>(Xop, M, Aop, a_rows, args, st, Aop2);
+}
+
+// The gated product of grouped rows: the token tile by the mean rows of an expert. (A tile
+// multiplies only the tokens its expert has, so an expert with fewer wastes no MMA work.)
+awq_status launch_silu_grouped(const void* X, int64_t T, const void* gate, const void* up,
+                               int64_t rows, const awq::TcArgs& args, cudaStream_t st) {
+  constexpr ASrc kA = ASrc::kPair16;
+  constexpr Epi kE = Epi::kSiluMul;
+  const int64_t mean = (T + args.E - 1) / args.E;
+  if (mean <= 32) return launch_tc<32, kA, kE, false, true>(X, T, gate, rows, args, st, up);
+  if (mean <= 64) return launch_tc<64, kA, kE, false, true>(X, T, gate, rows, args, st, up);
+  if (mean <= 128) return launch_tc<128, kA, kE, false, true>(X, T, gate, rows, args, st, up);
+  return launch_tc<256, kA, kE, false, true>(X, T, gate, rows, args, st, up);
 }
 
 // Streaming decode GEMM (M <= 16), launched with programmatic dependent launch.
@@ -238,15 +241,16 @@ bool gemv_stream_fits(int64_t M, int64_t N, int64_t K) {
   return gemv_config(M, N, K, &l);
 }
 
-template <int kNTiles, bool kOffset, bool kBf16, int kBits>
+template <int kNTiles, bool kOffset, bool kBf16, int kBits, bool kFused>
 awq_status launch_gemv_stream_t(const void* x, int64_t M, const uint32_t* qweight,
                                 const __half* scales, const uint8_t* zeros, int64_t N, int64_t K,
-                                const float* inv_s, unsigned flags, void* y, cudaStream_t st) {
+                                const float* inv_s, unsigned flags, void* y, cudaStream_t st,
+                                const awq::FusedEpi& epi) {
   using A = awq::act_t<kBf16>;
   static std::atomic<bool> attr_set[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return AWQ_ERR_CUDA;
-  auto kern = awq::gemv_stream_kernel<kNTiles, kOffset, kBf16, kBits>;
+  auto kern = awq::gemv_stream_kernel<kNTiles, kOffset, kBf16, kBits, kFused>;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) !=
         cudaSuccess)
@@ -284,42 +288,44 @@ awq_status launch_gemv_stream_t(const void* x, int64_t M, const uint32_t* qweigh
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kern, tw, ts, tz, static_cast<const A*>(x),
                          static_cast<int>(M), N, K, inv_s, static_cast<A*>(y), lay,
-                         flags) != cudaSuccess)
+                         flags, epi) != cudaSuccess)
     return AWQ_ERR_CUDA;
   return launch_status();
 }
 
-template <bool kBf16, int kBits>
+template <bool kBf16, int kBits, bool kFused>
 awq_status launch_gemv_stream_m(const void* x, int64_t M, const uint32_t* qweight,
                                 const __half* scales, const uint8_t* zeros, int64_t N, int64_t K,
-                                const float* inv_s, unsigned flags, void* y, cudaStream_t st) {
+                                const float* inv_s, unsigned flags, void* y, cudaStream_t st,
+                                const awq::FusedEpi& epi) {
   if (M == 1)
-    return launch_gemv_stream_t<1, true, kBf16, kBits>(x, M, qweight, scales, zeros, N, K, inv_s,
-                                                       flags, y, st);
+    return launch_gemv_stream_t<1, true, kBf16, kBits, kFused>(x, M, qweight, scales, zeros, N, K,
+                                                               inv_s, flags, y, st, epi);
   if (M <= 8)
-    return launch_gemv_stream_t<1, false, kBf16, kBits>(x, M, qweight, scales, zeros, N, K,
-                                                        inv_s, flags, y, st);
-  return launch_gemv_stream_t<2, false, kBf16, kBits>(x, M, qweight, scales, zeros, N, K, inv_s,
-                                                      flags, y, st);
+    return launch_gemv_stream_t<1, false, kBf16, kBits, kFused>(x, M, qweight, scales, zeros, N, K,
+                                                                inv_s, flags, y, st, epi);
+  return launch_gemv_stream_t<2, false, kBf16, kBits, kFused>(x, M, qweight, scales, zeros, N, K,
+                                                              inv_s, flags, y, st, epi);
 }
 
 // Returns AWQ_ERR_UNSUPPORTED when the shape does not suit the streaming kernel; the caller
 // then uses the register-streaming kernel (fp16, 4-bit, M <= 8) or the tensor-core path.
+template <bool kFused = false>
 awq_status launch_gemv_stream(const void* x, int64_t M, const uint32_t* qweight,
                               const __half* scales, const uint8_t* zeros, int64_t N, int64_t K,
                               int bits, const float* inv_s, unsigned flags, void* y,
-                              cudaStream_t st) {
+                              cudaStream_t st, const awq::FusedEpi& epi = {}) {
   if (!gemv_stream_fits(M, N, K)) return AWQ_ERR_UNSUPPORTED;
   const bool bf16 = (flags & AWQ_GEMM_BF16) != 0;
   if (bits == 3)
-    return bf16 ? launch_gemv_stream_m<true, 3>(x, M, qweight, scales, zeros, N, K, inv_s, flags,
-                                                y, st)
-                : launch_gemv_stream_m<false, 3>(x, M, qweight, scales, zeros, N, K, inv_s, flags,
-                                                 y, st);
-  return bf16 ? launch_gemv_stream_m<true, 4>(x, M, qweight, scales, zeros, N, K, inv_s, flags, y,
-                                              st)
-              : launch_gemv_stream_m<false, 4>(x, M, qweight, scales, zeros, N, K, inv_s, flags,
-                                               y, st);
+    return bf16 ? launch_gemv_stream_m<true, 3, kFused>(x, M, qweight, scales, zeros, N, K, inv_s,
+                                                        flags, y, st, epi)
+                : launch_gemv_stream_m<false, 3, kFused>(x, M, qweight, scales, zeros, N, K, inv_s,
+                                                         flags, y, st, epi);
+  return bf16 ? launch_gemv_stream_m<true, 4, kFused>(x, M, qweight, scales, zeros, N, K, inv_s,
+                                                      flags, y, st, epi)
+              : launch_gemv_stream_m<false, 4, kFused>(x, M, qweight, scales, zeros, N, K, inv_s,
+                                                       flags, y, st, epi);
 }
 
 int tc_bn_for(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
@@ -838,9 +844,176 @@ awq_status awq_gemm_w4a16(const awq_f16* X, int64_t M, const uint32_t* qweight,
   return launch_status();
 }
 
+}  // extern "C"
+
 // ------------------------------------------------------------------ fused epilogue, experts
 namespace {
 bool bad_ptr16(const void* p) { return p != nullptr && !aligned16(p); }
+
+template <typename... KArgs, typename... Args>
+awq_status launch_pdl(void (*kern)(KArgs...), dim3 grid, int threads, int smem, cudaStream_t st,
+                      Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return AWQ_ERR_CUDA;
+  return launch_status();
+}
+
+// Which product kernel a call takes, from its shape alone, and the streaming kernel's variant.
+struct FusedPlan {
+  enum Kind { kDecode, kStream, kTensor } kind;
+  int rb, xrows, slots;   // kStream
+  size_t workspace;
+};
+
+template <int kRB, bool kBf16, int kBits>
+awq_status launch_stream(const FusedPlan& plan, const void* X, const float* inv_s,
+                         const uint32_t* qweight, awq::StreamArgs a, void* workspace,
+                         cudaStream_t st) {
+  using L = awq::SfLayout<kRB>;
+  static std::atomic<bool> attr_set[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return AWQ_ERR_CUDA;
+  auto kern = awq::stream_fused_kernel<kRB, kBf16, kBits>;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) !=
+        cudaSuccess)
+      return AWQ_ERR_CUDA;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  constexpr int kRows = awq::kGemvRows * kRB;
+  a.xrows = plan.xrows;
+  a.slots = plan.slots;
+  CUtensorMap tw;
+  if (!make_tmap_2d(&tw, qweight, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.E * a.N, a.K * kBits / 32,
+                    kRows, 32, true))
+    return AWQ_ERR_CUDA;
+  // X in the kernel's layout first, in the workspace
+  const awq_status r = launch_pdl(
+      awq::prepare_rows_kernel<kBf16>, dim3(static_cast<unsigned>(a.T)), awq::kPrepThreads, 0, st,
+      static_cast<const uint4*>(X), a.T, a.K, inv_s, a.offsets, a.E, L::kChunkG, L::kXChunk,
+      static_cast<uint8_t*>(workspace));
+  if (r != AWQ_OK) return r;
+  a.xprep = static_cast<const uint8_t*>(workspace);
+  // at most this many tiles: T rows in blocks of xrows, one more for each expert with rows
+  const int64_t blocks = a.offsets == nullptr ? (a.T + a.xrows - 1) / a.xrows
+                                              : a.T / a.xrows + (a.T < a.E ? a.T : a.E);
+  const int64_t tiles = (a.N + kRows - 1) / kRows * blocks;
+  const int smem = L::total(a.slots, a.xrows, a.E);
+  const int64_t ctas = static_cast<int64_t>(num_sms()) * (smem <= kCoResidentSmem ? 2 : 1);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(tiles < ctas ? tiles : ctas)), awq::kG4Threads,
+                    smem, st, tw, a);
+}
+
+template <bool kBf16, int kBits>
+awq_status launch_stream_plan(const FusedPlan& p, const void* X, const float* inv_s,
+                              const uint32_t* qweight, const awq::StreamArgs& a, void* ws,
+                              cudaStream_t st) {
+  if (p.rb == 4) return launch_stream<4, kBf16, kBits>(p, X, inv_s, qweight, a, ws, st);
+  if (p.rb == 2) return launch_stream<2, kBf16, kBits>(p, X, inv_s, qweight, a, ws, st);
+  return launch_stream<1, kBf16, kBits>(p, X, inv_s, qweight, a, ws, st);
+}
+
+template <int kRB>
+void plan_stream(FusedPlan& p, int64_t T, int64_t E, int64_t K) {
+  using L = awq::SfLayout<kRB>;
+  p.kind = FusedPlan::kStream;
+  p.rb = kRB;
+  p.slots = awq::kSfMaxSlots;
+  for (int budget : {kCoResidentSmem, kSmemLimit}) {
+    p.slots = awq::kSfMaxSlots;
+    while (p.slots >= 2 && L::total(p.slots, p.xrows, static_cast<int>(E)) > budget) --p.slots;
+    if (p.slots >= 2) break;
+  }
+  const int64_t chunks = (K / awq::kGroup + L::kChunkG - 1) / L::kChunkG;
+  p.workspace = align256(static_cast<size_t>(T) * (chunks * L::kXChunk + sizeof(float)));
+}
+
+// The decode kernel (one launch, no workspace) for the shortest dense calls: at M = 1, 4 and 8 it
+// took 5.6, 7.0 and 8.6 us on [4096, 4096] where the streaming kernel behind its preparation
+// took 6.6, 9.1 and 9.4; on [11008, 4096] they are equal (12.3 and 12.4 at M = 1, 14.1 and 13.5
+// at 8), on [4096, 11008] the streaming kernel is faster at M = 8 (16.9 against 20.2).
+// The streaming kernel up to 8 rows of an expert on average: 8 experts of [14336, 4096] with 64
+// rows took 80 us there and 100 on the tensor-core kernel, with 128 rows 138 (in blocks of 16
+// tokens) and 101.
+FusedPlan fused_plan(int64_t T, int64_t E, int64_t N, int64_t K, bool grouped) {
+  FusedPlan p{};
+  if (!grouped && (T <= 2 || (T <= 8 && N <= (int64_t{1} << 25) / K)) && gemv_stream_fits(T, N, K)) {
+    p.kind = FusedPlan::kDecode;
+    return p;
+  }
+  if (T <= 8 * E) {
+    p.xrows = static_cast<int>(T < 8 ? T : 8);
+    const int64_t blocks = grouped ? T / p.xrows + (T < E ? T : E) : 1;
+    // 64 weight rows a tile read the tokens least often; 32 with few tokens (one token of two
+    // experts [14336, 4096]: 18.7 us against 20.0), and fewer where there are too few tiles
+    int rb = p.xrows <= 4 ? 2 : 4;
+    while (rb > 1 && (N + 16 * rb - 1) / (16 * rb) * blocks < num_sms()) rb /= 2;
+    if (rb == 4) plan_stream<4>(p, T, E, K);
+    else if (rb == 2) plan_stream<2>(p, T, E, K);
+    else plan_stream<1>(p, T, E, K);
+    return p;
+  }
+  p.kind = FusedPlan::kTensor;
+  const int splits = grouped ? 1 : splitk_for(T, N, K);
+  p.workspace = splits > 1 ? align256(static_cast<size_t>(splits) * T * N * sizeof(float)) : 0;
+  return p;
+}
+
+template <int BN, bool kBf16, int kBits>
+awq_status launch_tensor_bn(const void* X, const uint32_t* qweight, awq::TcArgs a, int early,
+                            cudaStream_t st) {
+  using L = awq::TfLayout<BN, kBits>;
+  static std::atomic<bool> attr_set[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return AWQ_ERR_CUDA;
+  auto kern = awq::tc_fused_kernel<BN, kBf16, kBits>;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem) !=
+        cudaSuccess)
+      return AWQ_ERR_CUDA;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  CUtensorMap tx, tw;
+  if (!make_tmap_2d(&tx, X, kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                    2, a.M, a.K, BN, awq::kTcBK, true) ||
+      !make_tmap_2d(&tw, qweight, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.E * a.N, a.K * kBits / 32,
+                    awq::kTcBM, L::kRowBytes / 4, kBits == 4))
+    return AWQ_ERR_CUDA;
+  a.row_tiles = static_cast<int>((a.N + awq::kTcBM - 1) / awq::kTcBM);
+  const int64_t tiles = a.offsets == nullptr ? (a.M + BN - 1) / BN
+                                             : a.M / BN + (a.M < a.E ? a.M : a.E);
+  const int64_t units = a.row_tiles * tiles * a.k_splits;
+  if (units > kMaxDim) return AWQ_ERR_INVALID_ARG;   // the kernel counts them in 32 bits
+  const int64_t sms = num_sms();
+  return launch_pdl(kern, dim3(static_cast<unsigned>(units < sms ? units : sms)), awq::kTfThreads,
+                    L::kSmem, st, tx, tw, a, early);
+}
+
+int tensor_bn(int64_t T, int64_t E) {
+  const int64_t mean = (T + E - 1) / E;
+  return mean <= 32 ? 32 : mean <= 64 ? 64 : mean <= 128 ? 128 : 192;
+}
+
+template <bool kBf16, int kBits>
+awq_status launch_tensor(const void* X, const uint32_t* qweight, const awq::TcArgs& a, int early,
+                         cudaStream_t st) {
+  switch (tensor_bn(a.M, a.E)) {
+    case 32: return launch_tensor_bn<32, kBf16, kBits>(X, qweight, a, early, st);
+    case 64: return launch_tensor_bn<64, kBf16, kBits>(X, qweight, a, early, st);
+    case 128: return launch_tensor_bn<128, kBf16, kBits>(X, qweight, a, early, st);
+    default: return launch_tensor_bn<192, kBf16, kBits>(X, qweight, a, early, st);
+  }
+}
 
 // What the products with a fused epilogue share: argument checks past the shapes, and the
 // launch. E experts with N rows each; offsets NULL for one expert with every row of X.
@@ -862,13 +1035,34 @@ awq_status fused_gemm(const void* X, int64_t T, const int32_t* offsets, int64_t 
       !aligned16(Y) || bad_ptr16(inv_s) || bad_ptr16(bias) || bad_ptr16(mul) ||
       bad_ptr16(residual))
     return AWQ_ERR_INVALID_ARG;
-  // TMA coordinates (weight rows, scale rows) are 32-bit
-  if (E * N > kMaxDim || E * (K / awq::kGroup) > kMaxDim) return AWQ_ERR_INVALID_ARG;
-  const int splits = offsets == nullptr ? splitk_for(T, N, K) : 1;
-  const size_t part_bytes =
-      splits > 1 ? align256(static_cast<size_t>(splits) * T * N * sizeof(float)) : 0;
-  if (part_bytes > 0 && (!workspace || ws_bytes < part_bytes || !aligned16(workspace)))
+  // TMA coordinates (weight rows, scale rows) and indices of scales are 32-bit
+  if (E * N > kMaxDim || E * (K / awq::kGroup) > kMaxDim / N) return AWQ_ERR_INVALID_ARG;
+  const bool bf16 = (flags & AWQ_GEMM_BF16) != 0;
+  const awq::FusedEpi epi{bias, mul, residual, act};
+  const FusedPlan plan = fused_plan(T, E, N, K, offsets != nullptr);
+  if (plan.workspace > 0 && (!workspace || ws_bytes < plan.workspace || !aligned16(workspace)))
     return AWQ_ERR_WORKSPACE;
+  if (plan.kind == FusedPlan::kDecode)
+    return launch_gemv_stream<true>(X, T, qweight, reinterpret_cast<const __half*>(scales), zeros,
+                                    N, K, bits, inv_s, flags, Y, st, epi);
+  if (plan.kind == FusedPlan::kStream) {
+    awq::StreamArgs a{};
+    a.N = N;
+    a.K = K;
+    a.T = static_cast<int>(T);
+    a.E = static_cast<int>(E);
+    a.offsets = offsets;
+    a.scales = reinterpret_cast<const __half*>(scales);
+    a.zeros = zeros;
+    a.epi = epi;
+    a.Y = Y;
+    if (bf16)
+      return bits == 3 ? launch_stream_plan<true, 3>(plan, X, inv_s, qweight, a, workspace, st)
+                       : launch_stream_plan<true, 4>(plan, X, inv_s, qweight, a, workspace, st);
+    return bits == 3 ? launch_stream_plan<false, 3>(plan, X, inv_s, qweight, a, workspace, st)
+                     : launch_stream_plan<false, 4>(plan, X, inv_s, qweight, a, workspace, st);
+  }
+  const int splits = offsets == nullptr ? splitk_for(T, N, K) : 1;
   awq::TcArgs args{};
   args.M = T;
   args.N = N;
@@ -882,18 +1076,15 @@ awq_status fused_gemm(const void* X, int64_t T, const int32_t* offsets, int64_t 
   args.inv_s = inv_s;
   args.offsets = offsets;
   args.E = static_cast<int>(E);
-  args.bias = bias;
-  args.mul = mul;
-  args.residual = residual;
-  args.act = act;
-  const bool bf16 = (flags & AWQ_GEMM_BF16) != 0;
+  args.epi = epi;
   awq_status r;
+  const int early = offsets == nullptr && (flags & AWQ_GEMM_WEIGHTS_READY) != 0;
   if (bf16)
-    r = bits == 3 ? launch_tc_grouped<ASrc::kPacked3, Epi::kFused, true>(X, T, qweight, E * N, args, st)
-                  : launch_tc_grouped<ASrc::kPacked4, Epi::kFused, true>(X, T, qweight, E * N, args, st);
+    r = bits == 3 ? launch_tensor<true, 3>(X, qweight, args, early, st)
+                  : launch_tensor<true, 4>(X, qweight, args, early, st);
   else
-    r = bits == 3 ? launch_tc_grouped<ASrc::kPacked3, Epi::kFused>(X, T, qweight, E * N, args, st)
-                  : launch_tc_grouped<ASrc::kPacked4, Epi::kFused>(X, T, qweight, E * N, args, st);
+    r = bits == 3 ? launch_tensor<false, 3>(X, qweight, args, early, st)
+                  : launch_tensor<false, 4>(X, qweight, args, early, st);
   if (r != AWQ_OK || splits == 1) return r;
   const unsigned grid = static_cast<unsigned>((T * N + 255) / 256);
   if (bf16) awq::splitk_fused_kernel<true><<<grid, 256, 0, st>>>(args);
@@ -907,11 +1098,12 @@ bool bad_groups(int64_t E, const int32_t* offsets) {
 }
 }  // namespace
 
+extern "C" {
+
 size_t awq_gemm_epilogue_workspace_size(int64_t M, int64_t N, int64_t K, int bits) {
   if (M <= 0 || K <= 0 || N <= 0) return 0;
   (void)bits;
-  const int splits = splitk_for(M, N, K);
-  return splits > 1 ? align256(static_cast<size_t>(splits) * M * N * sizeof(float)) : 0;
+  return fused_plan(M, 1, N, K, false).workspace;
 }
 
 awq_status awq_gemm_w4a16_epilogue(const awq_f16* X, int64_t M, const uint32_t* qweight,
@@ -926,8 +1118,10 @@ awq_status awq_gemm_w4a16_epilogue(const awq_f16* X, int64_t M, const uint32_t* 
 }
 
 size_t awq_gemm_grouped_workspace_size(int64_t T, int64_t E, int64_t N, int64_t K, int bits) {
-  (void)T; (void)E; (void)N; (void)K; (void)bits;
-  return 0;
+  if (T <= 0 || E <= 0 || K <= 0 || N <= 0) return 0;
+  (void)bits;
+  if (E > awq::kMaxExperts) return 0;
+  return fused_plan(T, E, N, K, true).workspace;
 }
 
 awq_status awq_gemm_w4a16_grouped(const awq_f16* X, int64_t T, const int32_t* offsets, int64_t E,
@@ -962,8 +1156,7 @@ awq_status awq_silu_mul_gemm_grouped(const awq_f16* X, int64_t T, const int32_t*
   args.k_splits = 1;
   args.offsets = offsets;
   args.E = static_cast<int>(E);
-  return launch_tc_grouped<ASrc::kPair16, Epi::kSiluMul>(
-      X, T, W_gate, E * I, args, static_cast<cudaStream_t>(stream), W_up);
+  return launch_silu_grouped(X, T, W_gate, W_up, E * I, args, static_cast<cudaStream_t>(stream));
 }
 
 // ------------------------------------------------------------------ act_stats of each expert

@@ -1,0 +1,612 @@
+// K7: W4A16 GEMM on the 5th-generation tensor cores with the fused epilogue, for one packed
+// weight or for rows grouped by expert.
+//
+// As in gemm_tc.cuh the MMA's M side is 128 weight rows and its N side up to BN tokens, with
+// the output in TMEM as 128 lanes (weight rows) x token columns, and the work units (expert, row
+// tile, token tile, K slice) go round the persistent CTAs. What differs is where the
+// dequantized weights go: not through shared memory but straight into TMEM, as the MMA's A
+// operand (lane = weight row, each 32-bit column two consecutive k). In gemm_tc.cuh a 128 x 128
+// group of weights costs shared memory a 32 KB write, a 32 KB read by the tensor core and, in
+// the packed reads, bank conflicts; with few tokens per weight that is what bounds it (1.7 TB/s
+// of packed weights at 16 to 64 tokens). Here a builder thread owns one weight row: it reads
+// the row's codes of a block without bank conflicts, dequantizes in registers and stores the
+// block's columns of its lane.
+//   warp 0       TMA producer of X
+//   warp 1       TMEM allocator and single-thread tcgen05.mma issuer
+//   warp 2       TMA producer of packed codes (and inv_s), prefetch of scales and zero points
+//   warp 3       idle
+//   warps 4..19  builders: four sets of four warps (a warp reaches the TMEM lanes of its quarter,
+//                warp % 4); the sets take the K blocks in turn, so that four chains of
+//                shared-memory reads, arithmetic, TMEM stores and barriers run at once
+//   warps 20..27 epilogue: two warps per quarter, each half of the token columns
+// A K block, the unit of the X and A pipelines, is 128 k (a group), or 64 k with BN = 192. TMEM:
+// two accumulators of BN columns and kNA A stages. BN stops at 192 so that both accumulators fit
+// beside four A stages and a tile's epilogue always overlaps the next tile's products. (A set's
+// turn comes round after four blocks, and a barrier's parity tells only neighbouring phases
+// apart: a stage must not come round sooner, so kNA >= the sets.)
+// Packed codes: 4 bits: boxes of 128 rows x 128 bytes (two groups) with the 128-byte swizzle;
+// 3 bits: one box of 3 or 5 groups (an odd multiple of 48 bytes per row, so that the 16-byte
+// reads of eight consecutive rows fall into eight different bank groups as they are).
+#pragma once
+#include "common.cuh"
+#include "fused.cuh"
+#include "gemm_tc.cuh"
+
+namespace awq {
+
+constexpr int kTfSets = 4;
+constexpr int kTfBuildWarp0 = 4;
+constexpr int kTfEpiWarp0 = kTfBuildWarp0 + 4 * kTfSets;
+constexpr int kTfThreads = (kTfEpiWarp0 + 8) * 32;
+
+template <int BN, int kBits>
+struct TfLayout {
+  static_assert(BN == 32 || BN == 64 || BN == 128 || BN == 192, "token tiles");
+  static constexpr int kHB = BN == 192 ? 1 : 2;                   // 64-k halves of a K block
+  static constexpr int kXHalf = BN * kTcBK * 2;
+  static constexpr int kXBytes = kHB * kXHalf;                    // a K block of X
+  static constexpr int kXStages = BN == 192 ? 5 : BN == 128 ? 3 : BN == 64 ? 4 : 6;
+  static constexpr int kACols = kHB * 32;                         // TMEM columns of an A stage
+  static constexpr int kNA = BN >= 128 ? 4 : 6;
+  static constexpr int kAccCol = 0;
+  static constexpr int kACol = 2 * BN;
+  static_assert(kACol + kNA * kACols <= 512 && kNA >= kTfSets, "TMEM columns");
+  static constexpr int kPG = kBits == 4 ? (BN == 192 ? 2 : 4) : (BN == 192 ? 3 : 5);
+  static constexpr int kRowBytes = kBits == 4 ? 128 : kPG * 48;   // of a box
+  static constexpr int kBoxes = kBits == 4 ? kPG / 2 : 1;
+  static constexpr int kBoxBytes = kTcBM * kRowBytes;
+  static constexpr int kPBytes = (kBoxes * kBoxBytes + 1023) / 1024 * 1024;
+  static constexpr int kInvBytes = kPG * kGroup * 4;
+  static constexpr int kBarBytes = 512;
+  static constexpr int kFit = (kTcSmemMax - 1024 - kBarBytes - static_cast<int>(sizeof(GroupTable)) -
+                               kXStages * kXBytes) / (kPBytes + kInvBytes);
+  static constexpr int kPSlots = kFit < 6 ? kFit : 6;
+  static_assert(kPSlots >= 2, "packed ring");
+  static constexpr int kPOff = kXStages * kXBytes;
+  static constexpr int kIOff = kPOff + kPSlots * kPBytes;
+  static constexpr int kBarOff = kIOff + kPSlots * kInvBytes;
+  static constexpr int kTabOff = kBarOff + kBarBytes;
+  static constexpr int kSmem = kTabOff + static_cast<int>(sizeof(GroupTable)) + 1024;
+  static_assert((2 * kXStages + 2 * kNA + 2 * kPSlots + 4) * 8 + 8 <= kBarBytes, "barriers");
+};
+
+// D[tmem] (+)= A[tmem] * B[smem desc]^T, 16-bit inputs, fp32 accumulator, one CTA.
+__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// mbar_wait for a warp that has time: it looks only now and then, so that its polling takes no
+// issue slots from the warps that set the pace.
+__device__ __forceinline__ bool mbar_wait_lazy(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+  for (int i = 0; i < 64; ++i) {
+    if (mbar_try_wait(a, parity)) return true;
+    __nanosleep(256);
+  }
+  return mbar_wait(bar, parity);
+}
+
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// 32 lanes x 16 consecutive 32-bit columns from registers (thread i: lane base + i).
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// A work unit: K slice, expert, row tile and token tile, and the slice's groups.
+struct TfUnit {
+  int e, row0, m0, cols;      // expert, first weight row, first token, its tokens (at most BN)
+  int g0, groups, ksplit;
+};
+// Unit u (32-bit: see the launch). Units of a slice sweep the token tiles of 16 row tiles at a
+// time (tile_of_block's order).
+template <int BN>
+__device__ __forceinline__ TfUnit tf_unit(unsigned u, const TcArgs& a, const GroupTable* tab, int G) {
+  TfUnit t;
+  const unsigned rt = static_cast<unsigned>(a.row_tiles);
+  const unsigned tiles = rt * static_cast<unsigned>(tab->tile[a.E]);
+  t.ksplit = 0;
+  if (a.k_splits > 1) {
+    t.ksplit = static_cast<int>(u / tiles);
+    u -= t.ksplit * tiles;
+  }
+  int lo = 0, n = a.E;   // the last expert that starts at or before the unit
+  while (n > 1) {
+    const int half = n >> 1;
+    if (rt * static_cast<unsigned>(tab->tile[lo + half]) <= u) {
+      lo += half;
+      n -= half;
+    } else {
+      n = half;
+    }
+  }
+  t.e = lo;
+  u -= rt * static_cast<unsigned>(tab->tile[lo]);
+  const unsigned mt = static_cast<unsigned>(tab->tile[lo + 1] - tab->tile[lo]);
+  const unsigned per = kTcRasterRows * mt;
+  const unsigned grp = u / per, in = u - grp * per;
+  const unsigned first = grp * kTcRasterRows;
+  const unsigned here = rt - first < kTcRasterRows ? rt - first : kTcRasterRows;
+  const unsigned m = in / here;
+  t.row0 = static_cast<int>(first + in - m * here) * kTcBM;
+  t.m0 = tab->off[lo] + static_cast<int>(m) * BN;
+  const int left = tab->off[lo + 1] - t.m0;
+  t.cols = left < BN ? left : BN;
+  t.g0 = static_cast<int>(static_cast<int64_t>(t.ksplit) * G / a.k_splits);
+  t.groups = static_cast<int>(static_cast<int64_t>(t.ksplit + 1) * G / a.k_splits) - t.g0;
+  return t;
+}
+
+// 32 weights (one 32-k quarter of a group: 4 words at 4 bits, 3 at 3 bits) of a row to 16 MMA
+// operand pairs: exact q - z, then the scale with one rounding to 16 bits. With bf16 the fp16
+// scale goes in as two bf16 parts, (q - z) hi + (q - z) lo, since rounding it to one would add an
+// error of the size of the product's own; inv_s (this quarter's) likewise from fp32.
+template <bool kBf16, int kBits>
+__device__ __forceinline__ void dequant32(const uint32_t* w, uint32_t z, uint32_t sc_hi,
+                                          uint32_t sc_lo, float scf, const float* inv,
+                                          uint32_t (&o)[16]) {
+  const uint32_t bias = ((kBf16 ? 0x4300u : 0x6400u) | z) * 0x00010001u;
+  if constexpr (kBits == 4) {
+    const __half2 hi = u32_as_h2((0xD400u | (z << 4)) * 0x00010001u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t v[4];
+      if constexpr (kBf16) dequant_word_qz_bf16(w[j], bias, v);
+      else dequant_word_qz(w[j], u32_as_h2(bias), hi, v);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) o[4 * j + q] = v[q];
+    }
+  } else {
+    o[0] = raw3_qz<0, 0, kBf16>(w[0], w[1], w[2], bias);
+    o[1] = raw3_qz<0, 1, kBf16>(w[0], w[1], w[2], bias);
+    o[2] = raw3_qz<0, 2, kBf16>(w[0], w[1], w[2], bias);
+    o[3] = raw3_qz<0, 3, kBf16>(w[0], w[1], w[2], bias);
+    o[4] = raw3_qz<1, 0, kBf16>(w[0], w[1], w[2], bias);
+    o[5] = raw3_qz<1, 1, kBf16>(w[0], w[1], w[2], bias);
+    o[6] = raw3_qz<1, 2, kBf16>(w[0], w[1], w[2], bias);
+    o[7] = raw3_qz<1, 3, kBf16>(w[0], w[1], w[2], bias);
+    o[8] = raw3_qz<2, 0, kBf16>(w[0], w[1], w[2], bias);
+    o[9] = raw3_qz<2, 1, kBf16>(w[0], w[1], w[2], bias);
+    o[10] = raw3_qz<2, 2, kBf16>(w[0], w[1], w[2], bias);
+    o[11] = raw3_qz<2, 3, kBf16>(w[0], w[1], w[2], bias);
+    o[12] = raw3_qz<3, 0, kBf16>(w[0], w[1], w[2], bias);
+    o[13] = raw3_qz<3, 1, kBf16>(w[0], w[1], w[2], bias);
+    o[14] = raw3_qz<3, 2, kBf16>(w[0], w[1], w[2], bias);
+    o[15] = raw3_qz<3, 3, kBf16>(w[0], w[1], w[2], bias);
+  }
+  if (inv == nullptr) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if constexpr (kBf16)
+        o[j] = b2_as_u32(__hfma2(u32_as_b2(o[j]), u32_as_b2(sc_hi),
+                                 __hmul2(u32_as_b2(o[j]), u32_as_b2(sc_lo))));
+      else
+        o[j] = h2_as_u32(__hmul2(u32_as_h2(o[j]), u32_as_h2(sc_hi)));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float4 s = reinterpret_cast<const float4*>(inv)[j];
+      float2 f = act2_to_float2<kBf16>(o[2 * j]);
+      o[2 * j] = float2_to_act2<kBf16>(f.x * (scf * s.x), f.y * (scf * s.y));
+      f = act2_to_float2<kBf16>(o[2 * j + 1]);
+      o[2 * j + 1] = float2_to_act2<kBf16>(f.x * (scf * s.z), f.y * (scf * s.w));
+    }
+  }
+}
+
+// 8 token columns of one weight row through the epilogue, the activation known at compile
+// time: loads first, then arithmetic, then stores. y: the row's first output of the columns.
+template <bool kBf16, int kAct>
+__device__ __forceinline__ void fused_columns(const FusedEpi& f, act_t<kBf16>* Y, int64_t y, int64_t N,
+                                              int cols, float bias, const uint32_t* v) {
+  using A = act_t<kBf16>;
+  A mul[8], res[8];
+  const A* pm = static_cast<const A*>(f.mul);
+  const A* pr = static_cast<const A*>(f.residual);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    mul[j] = pm != nullptr && j < cols ? pm[y + j * N] : A(1.0f);
+    res[j] = pr != nullptr && j < cols ? pr[y + j * N] : A(0.0f);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float p = activate(__uint_as_float(v[j]) + bias, kAct);
+    if (j < cols)
+      Y[y + j * N] = float_to_act<kBf16>(fmaf(p, act_to_float<kBf16>(mul[j]), act_to_float<kBf16>(res[j])));
+  }
+}
+
+template <int BN, bool kBf16, int kBits>
+__global__ void __launch_bounds__(kTfThreads, 1)
+    tc_fused_kernel(const __grid_constant__ CUtensorMap tmap_x,
+                    const __grid_constant__ CUtensorMap tmap_w, const TcArgs args, const int early) {
+  using L = TfLayout<BN, kBits>;
+  constexpr int NX = L::kXStages, NA = L::kNA, P = L::kPSlots, kPG = L::kPG;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  uint64_t* xfull = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* xempty = xfull + NX;
+  uint64_t* afull = xempty + NX;
+  uint64_t* aempty = afull + NA;
+  uint64_t* pfull = aempty + NA;
+  uint64_t* pempty = pfull + P;
+  uint64_t* dfull = pempty + P;
+  uint64_t* dempty = dfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dempty + 2);
+  GroupTable* tab = reinterpret_cast<GroupTable*>(smem + L::kTabOff);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int G = static_cast<int>(args.K / kGroup);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NX; ++i) {
+      mbar_init(&xfull[i], 1);
+      mbar_init(&xempty[i], 1);
+    }
+    for (int i = 0; i < NA; ++i) {
+      mbar_init(&afull[i], 4);    // the warps of a builder set
+      mbar_init(&aempty[i], 1);
+    }
+    for (int i = 0; i < P; ++i) {
+      mbar_init(&pfull[i], 1);
+      mbar_init(&pempty[i], 4 * kTfSets);   // every builder warp
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&dfull[i], 1);
+      mbar_init(&dempty[i], 8);   // every epilogue warp
+    }
+    fence_barrier_init();
+    tma_prefetch_desc(&tmap_x);
+    tma_prefetch_desc(&tmap_w);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  // With `early` (one weight, not written by the preceding kernel) only what that kernel may
+  // have written waits for it: X, mul, residual, Y, partial sums.
+  if (!early) pdl_wait();
+  if (warp == 0) build_group_table(tab->off, tab->tile, args.offsets, args.E, args.M, BN);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const unsigned units = static_cast<unsigned>(args.row_tiles) *
+                         static_cast<unsigned>(tab->tile[args.E]) * args.k_splits;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ X producer
+    pdl_wait();
+    pdl_launch_dependents();
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (unsigned u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        const TfUnit t = tf_unit<BN>(u, args, tab, G);
+        const int blocks = 2 * t.groups / L::kHB;
+        for (int i = 0; i < blocks; ++i) {
+          ok = mbar_wait(&xempty[s], ph ^ 1);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&xfull[s], L::kXBytes);
+#pragma unroll
+          for (int h = 0; h < L::kHB; ++h)
+            tma_load_2d(smem + s * L::kXBytes + h * L::kXHalf, &tmap_x, &xfull[s],
+                        (2 * t.g0 + i * L::kHB + h) * kTcBK, t.m0);
+          if (++s == NX) { s = 0; ph ^= 1; }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    // The whole warp walks the loop, so that what the instructions take (descriptors, TMEM
+    // addresses) is the same in every lane and lives in uniform registers; one elected lane
+    // issues. (A loop that only lane 0 ran issued one MMA in about 80 cycles, whatever its N.)
+    int s = 0, as = 0, buf = 0;
+    uint32_t ph = 0, aph = 0, dph = 0;
+    bool ok = true;
+    for (unsigned u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const TfUnit t = tf_unit<BN>(u, args, tab, G);
+      const int blocks = 2 * t.groups / L::kHB;
+      // a tile multiplies only the tokens it has (N goes in steps of 16): the rest of its BN rows
+      // of X belong to another expert or lie past the end
+      const uint32_t idesc = f16_idesc(kTcBM, (t.cols + 15) / 16 * 16, kBf16);
+      const uint32_t d = tmem + L::kAccCol + buf * BN;
+      ok = __all_sync(0xffffffffu, mbar_wait(&dempty[buf], dph ^ 1));   // the epilogue has read it
+      for (int i = 0; i < blocks && ok; ++i) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&afull[as], aph) && mbar_wait(&xfull[s], ph));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t xd = sw128_kmajor_desc(smem_u32(smem) + s * L::kXBytes);
+        const uint32_t a = tmem + L::kACol + as * L::kACols;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4 * L::kHB; ++k)   // 16 k each: 8 columns of A, 32 bytes of X
+            tc_mma_f16_ta(d, a + 8 * k, xd + (k >> 2) * (L::kXHalf >> 4) + 2 * (k & 3), idesc,
+                          (i | k) != 0 ? 1u : 0u);
+          tc_commit(&xempty[s]);
+          tc_commit(&aempty[as]);
+          if (i == blocks - 1) tc_commit(&dfull[buf]);
+        }
+        __syncwarp();
+        if (++s == NX) { s = 0; ph ^= 1; }
+        if (++as == NA) { as = 0; aph ^= 1; }
+      }
+      if (++buf == 2) { buf = 0; dph ^= 1; }
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ packed producer
+    int ps = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (unsigned u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const TfUnit t = tf_unit<BN>(u, args, tab, G);
+      for (int i = 0; i < t.groups; i += kPG) {   // a slot holds kPG groups of a unit
+        ok = __all_sync(0xffffffffu, mbar_wait(&pempty[ps], ph ^ 1));
+        if (!ok) break;
+        const int g = t.g0 + i;
+        if (lane == 0) {
+          // groups past K are zero codes that nothing uses; a box is always counted whole
+          const int32_t arow = static_cast<int32_t>(t.e * args.N) + t.row0;
+          const uint32_t inv_bytes =
+              args.inv_s == nullptr
+                  ? 0u : static_cast<uint32_t>((G - g < kPG ? G - g : kPG) * kGroup * 4);
+          mbar_arrive_expect_tx(&pfull[ps], L::kBoxes * L::kBoxBytes + inv_bytes);
+#pragma unroll
+          for (int b = 0; b < L::kBoxes; ++b)
+            tma_load_2d(smem + L::kPOff + ps * L::kPBytes + b * L::kBoxBytes, &tmap_w, &pfull[ps],
+                        kBits == 4 ? (g + 2 * b) * 16 : g * 12, arow);
+          if (inv_bytes != 0 && AWQ_IN_BOUNDS(g < G))
+            bulk_load_1d(smem + L::kIOff + ps * L::kInvBytes,
+                         args.inv_s + (static_cast<int64_t>(t.e) * G + g) * kGroup, inv_bytes,
+                         &pfull[ps]);
+        }
+        // scales (256 bytes a group) and zero points (128) of the slot towards L2
+        const int pg = g + lane / 4;
+        if (lane / 4 < kPG && pg < G) {
+          const int64_t n = t.row0 + (lane % 4 == 1 ? 64 : 0);
+          const int64_t x = (static_cast<int64_t>(t.e) * G + pg) * args.N + n;
+          if (n < args.N && lane % 4 < 3)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                lane % 4 < 2 ? static_cast<const void*>(args.scales + x)
+                             : static_cast<const void*>(args.zeros + x)));
+        }
+        if (++ps == P) { ps = 0; ph ^= 1; }
+      }
+    }
+  } else if (warp >= kTfBuildWarp0 && warp < kTfEpiWarp0) {
+    // ------------------------------------------------------------------ builders
+    const int set = (warp - kTfBuildWarp0) >> 2;
+    const int row = 32 * (warp & 3) + lane;
+    const uint32_t ta = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + L::kACol;
+    constexpr int kPerG = 2 / L::kHB;   // K blocks of a group
+    const uint32_t N32 = static_cast<uint32_t>(args.N);
+    // scale and zero point of this thread's row (rows past N read the last one)
+    auto load_sz = [&](const TfUnit& t, int i, unsigned short& s, unsigned char& z) {   // of block i
+      uint32_t n = static_cast<uint32_t>(t.row0 + row);
+      n = n < N32 ? n : N32 - 1;
+      const uint32_t x = static_cast<uint32_t>(t.e * G + t.g0 + i / kPerG) * N32 + n;
+      s = reinterpret_cast<const unsigned short*>(args.scales)[x];
+      z = args.zeros[x];
+    };
+    unsigned short s_cur = 0, s_far = 0;   // of the block at hand; of the set's next block
+    unsigned char z_cur = 0, z_far = 0;
+    unsigned u = blockIdx.x;
+    TfUnit t{}, tn{};       // the unit at hand and the CTA's next one
+    if (u < units) t = tf_unit<BN>(u, args, tab, G);
+    int i = set;            // K block of the unit
+    int slot_i = 0;         // the ring's current slot is the unit's slot_i-th
+    int ps = 0, as = set % NA;
+    uint32_t ph = 0, aph = (set / NA) & 1;
+    // moves on to slot `to` of the unit: this warp is done with every slot before it (a slot none
+    // of whose groups the set has is awaited too, so that each arrival belongs to its filling)
+    auto release_to = [&](int to) {
+      bool ok = true;
+      for (; slot_i < to && ok; ++slot_i) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&pfull[ps], ph));
+        if (ok && lane == 0) mbar_arrive(&pempty[ps]);
+        if (++ps == P) { ps = 0; ph ^= 1; }
+      }
+      return ok;
+    };
+    bool ok = true;
+    // the first unit may have fewer blocks than the set's number
+    while (u < units && i >= kPerG * t.groups && ok) {
+      ok = release_to((t.groups + kPG - 1) / kPG);
+      slot_i = 0;
+      i -= kPerG * t.groups;
+      u += gridDim.x;
+      if (u < units) t = tf_unit<BN>(u, args, tab, G);
+    }
+    if (u < units) load_sz(t, i, s_far, z_far);
+    while (u < units && ok) {
+      // the set's next block: in this unit, or in the first later one that has it
+      unsigned un = u;
+      int in = i + kTfSets;
+      const bool same = in < kPerG * t.groups;
+      s_cur = s_far;
+      z_cur = z_far;
+      if (same) {
+        load_sz(t, in, s_far, z_far);
+      } else {
+        tn = t;
+        while (un < units && in >= kPerG * tn.groups) {
+          in -= kPerG * tn.groups;
+          un += gridDim.x;
+          if (un < units) tn = tf_unit<BN>(un, args, tab, G);
+        }
+        if (un < units) load_sz(tn, in, s_far, z_far);
+      }
+      {
+        const int gi = i / kPerG % kPG, h = i % kPerG;   // group of the slot, half of the group
+        ok = release_to(i / kPerG / kPG) &&
+             __all_sync(0xffffffffu, mbar_wait(&pfull[ps], ph) && mbar_wait(&aempty[as], aph ^ 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint8_t* box = smem + L::kPOff + ps * L::kPBytes;
+        const float* inv = args.inv_s == nullptr
+                               ? nullptr
+                               : reinterpret_cast<const float*>(smem + L::kIOff + ps * L::kInvBytes) +
+                                     gi * kGroup + h * kTcBK;
+        const float scf = __half2float(__ushort_as_half(s_cur));
+        uint32_t sc_hi, sc_lo = 0;
+        if constexpr (kBf16) {
+          const float hi = __bfloat162float(__float2bfloat16_rn(scf));
+          sc_hi = float2_to_act2<true>(hi, hi);
+          sc_lo = float2_to_act2<true>(scf - hi, scf - hi);
+        } else {
+          sc_hi = static_cast<uint32_t>(s_cur) * 0x00010001u;
+        }
+#pragma unroll
+        for (int hh = 0; hh < L::kHB; ++hh) {   // 64 k: 32 columns
+          uint32_t wd[2 * kBits];
+          const int hg = L::kHB == 2 ? hh : h;   // half of the group
+          if constexpr (kBits == 4) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const uint4 p = *reinterpret_cast<const uint4*>(
+                  box + (gi >> 1) * L::kBoxBytes + row * 128 +
+                  ((((gi & 1) * 4 + 2 * hg + q) ^ (row & 7)) << 4));
+              wd[4 * q] = p.x;
+              wd[4 * q + 1] = p.y;
+              wd[4 * q + 2] = p.z;
+              wd[4 * q + 3] = p.w;
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+              const uint2 p = *reinterpret_cast<const uint2*>(box + row * L::kRowBytes + gi * 48 +
+                                                              hg * 24 + q * 8);
+              wd[2 * q] = p.x;
+              wd[2 * q + 1] = p.y;
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t o[16];
+            dequant32<kBf16, kBits>(wd + q * kBits, z_cur, sc_hi, sc_lo, scf,
+                                    inv == nullptr ? nullptr : inv + 64 * hh + 32 * q, o);
+            tmem_st_32x32b_x16(ta + as * L::kACols + hh * 32 + q * 16, o);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&afull[as]);
+        if (same) ok = release_to(in / kPerG / kPG);   // the codes and factors have been read
+        as += kTfSets;
+        if (as >= NA) { as -= NA; aph ^= 1; }
+      }
+      if (!same) {   // the rest of this unit's slots, and those of units without a group of the set
+        while (u != un && ok) {
+          ok = release_to((t.groups + kPG - 1) / kPG);
+          slot_i = 0;
+          u += gridDim.x;
+          if (u < units) t = u == un ? tn : tf_unit<BN>(u, args, tab, G);
+          else break;
+        }
+        if (un >= units) break;
+      }
+      i = in;
+    }
+  } else if (warp >= kTfEpiWarp0) {
+    // ------------------------------------------------------------------ epilogue
+    pdl_wait();
+    using A = act_t<kBf16>;
+    const int half = (warp - kTfEpiWarp0) >> 2;
+    const int row = 32 * (warp & 3) + lane;
+    const uint32_t td = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + L::kAccCol;
+    int buf = 0;
+    uint32_t ph = 0;
+    for (unsigned u = blockIdx.x; u < units; u += gridDim.x) {
+      const TfUnit t = tf_unit<BN>(u, args, tab, G);
+      const int64_t n = t.row0 + row;
+      const int cols = t.cols;
+      const bool live = n < args.N && AWQ_IN_BOUNDS(t.m0 + cols <= args.M && t.e < args.E);
+      const float bias = live ? fused_bias<kBf16>(args.epi, t.e * args.N + n) : 0.0f;
+      if (!__all_sync(0xffffffffu, mbar_wait_lazy(&dfull[buf], ph))) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c0 = 16 * half; c0 < cols; c0 += 32) {   // the halves take alternate 16 columns
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(td + buf * BN + c0, v);
+        tmem_ld_wait();
+        const int nc = cols - c0 < 16 ? cols - c0 : 16;
+        const int64_t y = static_cast<int64_t>(t.m0 + c0) * args.N + n;
+        if (live) {
+          A* Y = static_cast<A*>(args.Y);
+          if (args.k_splits > 1) {
+            float* p = args.partial + static_cast<int64_t>(t.ksplit) * args.M * args.N + y;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (j < nc) p[j * args.N] = __uint_as_float(v[j]);
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 16; c += 8) {
+              const int64_t yc = y + c * args.N;
+              uint32_t w[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) w[j] = c ? v[8 + j] : v[j];
+              switch (args.epi.act) {
+                case kActRelu:
+                  fused_columns<kBf16, kActRelu>(args.epi, Y, yc, args.N, nc - c, bias, w);
+                  break;
+                case kActSilu:
+                  fused_columns<kBf16, kActSilu>(args.epi, Y, yc, args.N, nc - c, bias, w);
+                  break;
+                case kActGelu:
+                  fused_columns<kBf16, kActGelu>(args.epi, Y, yc, args.N, nc - c, bias, w);
+                  break;
+                case kActGeluTanh:
+                  fused_columns<kBf16, kActGeluTanh>(args.epi, Y, yc, args.N, nc - c, bias, w);
+                  break;
+                default:
+                  fused_columns<kBf16, kActNone>(args.epi, Y, yc, args.N, nc - c, bias, w);
+              }
+            }
+          }
+        }
+        __syncwarp();   // the next TMEM load is the whole warp's
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&dempty[buf]);
+      if (++buf == 2) { buf = 0; ph ^= 1; }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace awq

@@ -38,6 +38,7 @@
 // leave their loops so the CTA still releases its TMEM and exits.
 #pragma once
 #include "common.cuh"
+#include "fused.cuh"
 
 namespace awq {
 
@@ -70,17 +71,7 @@ enum class ASrc : int { kPacked4 = 0, kPacked3 = 1, kSplit16 = 2, kPair16 = 3, k
 // recombined two-part product; kSiluMul: fp16 H = silu(D_0) * D_1 of the two accumulators;
 // kStoreF32: the fp32 product itself (the Gram matrix); kGramDot: per-row sums of
 // D[n][j] * e'[n][j], the recombined product times the row's own error operand.
-// kFused: Y = act(D + bias) * mul + residual, each part optional (or fp32 split-K partials).
-enum class Epi : int { kStoreY = 0, kRowSumSq = 1, kSiluMul = 2, kStoreF32 = 3, kGramDot = 4,
-                       kFused = 5 };
-
-// Rows grouped by expert: expert e's rows are offsets[e] .. offsets[e + 1] - 1 of X and Y. The
-// offsets live on the device (a router wrote them), so each CTA makes its own table of them.
-constexpr int kMaxExperts = 1024;
-struct GroupTable {
-  int off[kMaxExperts + 1];    // first row of each expert, then the end of the last
-  int tile[kMaxExperts + 1];   // token tiles before each expert, then their total
-};
+enum class Epi : int { kStoreY = 0, kRowSumSq = 1, kSiluMul = 2, kStoreF32 = 3, kGramDot = 4 };
 
 template <int BN, ASrc kA, int kBlkT = 1, bool kGrp = false>
 struct TcLayout {
@@ -163,94 +154,9 @@ struct TcArgs {
   // grouped launches: M rows of X sorted by expert, N weight rows of each of the E experts
   const int* offsets;   // [E + 1], or NULL for one expert with every row
   int E;
-  // kFused epilogue, in the activations' type; NULL where the part is absent
-  const void* bias;     // [E, N]
-  const void* mul;      // [M, N]
-  const void* residual; // [M, N]
-  int act;              // Act
+  FusedEpi epi;         // of the fused products (gemm_fused.cuh)
 };
 
-// Activations of the fused epilogue (the values of AWQ_ACT_*).
-enum Act : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
-
-// act(v) in fp32. A NaN stays one (relu as well); silu and gelu as their formulas give it.
-__device__ __forceinline__ float activate(float v, int act) {
-  switch (act) {
-    case kActRelu: return v < 0.0f ? 0.0f : v;
-    case kActSilu: return __fdiv_rn(v, 1.0f + expf(-v));
-    case kActGelu: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-    case kActGeluTanh:   // sqrt(2 / pi) (v + 0.044715 v^3)
-      return 0.5f * v * (1.0f + tanhf(0.79788456080286536f * fmaf(0.044715f * v * v, v, v)));
-    default: return v;
-  }
-}
-
-// The fused epilogue of output (m, n) of expert e: act(v + bias) * mul + residual, in fp32
-// with one rounding at the end. mul and residual are read by the thread that writes Y, before
-// it does, so either may be Y itself.
-template <bool kBf16>
-__device__ __forceinline__ float act_to_float(act_t<kBf16> v) {
-  if constexpr (kBf16) return __bfloat162float(v);
-  else return __half2float(v);
-}
-template <bool kBf16>
-__device__ __forceinline__ float fused_bias(const TcArgs& a, int e, int64_t n) {
-  return a.bias == nullptr ? 0.0f
-                           : act_to_float<kBf16>(static_cast<const act_t<kBf16>*>(
-                                 a.bias)[static_cast<int64_t>(e) * a.N + n]);
-}
-template <bool kBf16>
-__device__ __forceinline__ void fused_store(const TcArgs& a, int64_t m, int64_t n, float v) {
-  using A = act_t<kBf16>;
-  const int64_t i = m * a.N + n;
-  v = activate(v, a.act);
-  if (a.mul != nullptr) v *= act_to_float<kBf16>(static_cast<const A*>(a.mul)[i]);
-  if (a.residual != nullptr) v += act_to_float<kBf16>(static_cast<const A*>(a.residual)[i]);
-  static_cast<A*>(a.Y)[i] = float_to_act<kBf16>(v);
-}
-
-// Fills the table from args.offsets (one warp). An offset outside 0 .. M, or below one before
-// it, is taken as the nearest value in order, so no row outside X and Y is ever touched.
-__device__ __forceinline__ void build_group_table(GroupTable& t, const TcArgs& a, int bn) {
-  const int lane = threadIdx.x & 31;
-  const int M = static_cast<int>(a.M);
-  if (a.offsets == nullptr) {
-    if (lane == 0) {
-      t.off[0] = 0;
-      t.off[1] = M;
-      t.tile[0] = 0;
-      t.tile[1] = (M + bn - 1) / bn;
-    }
-    return;
-  }
-  int high = 0, tiles = 0;   // the last offset so far, the tiles before it
-  for (int base = 0; base <= a.E; base += 32) {
-    const int e = base + lane;
-    int v = e <= a.E ? a.offsets[e] : 0;
-    v = v < 0 ? 0 : v > M ? M : v;
-    if (lane == 0 && v < high) v = high;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int w = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o && w > v) v = w;
-    }
-    const int before = __shfl_up_sync(0xffffffffu, v, 1);
-    // tiles of expert e - 1 end where expert e's begin
-    const int rows = e == 0 || e > a.E ? 0 : v - (lane == 0 ? high : before);
-    int sum = (rows + bn - 1) / bn;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int w = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += w;
-    }
-    if (e <= a.E) {
-      t.off[e] = v;
-      t.tile[e] = tiles + sum;
-    }
-    high = __shfl_sync(0xffffffffu, v, 31);
-    tiles += __shfl_sync(0xffffffffu, sum, 31);
-  }
-}
 
 // Grouped tile order: consecutive work units sweep the token tiles of a group of
 // kTcRasterRows weight-row tiles, so the units in flight at one time share a few A tiles and
@@ -385,50 +291,6 @@ __device__ __forceinline__ uint32_t dequant3_pair(uint32_t w0, uint32_t w1, uint
   else return h2_as_u32(__hmul2(u32_as_h2(qz), u32_as_h2(sc2u)));
 }
 
-// Four exact (q - z) pairs times scale * inv_s[k], the products in fp32 with one rounding to
-// 16 bits at the end. (A factor rounded to 16 bits before the product, as pair_scales makes
-// it, rounds twice: with the output's own rounding that is sqrt(3) of the error of a product
-// in fp32, against sqrt(2) here.)
-template <bool kBf16>
-__device__ __forceinline__ uint4 scale_inv8(uint4 qz, float scale, const float* inv_s) {
-  const float4 a = *reinterpret_cast<const float4*>(inv_s);
-  const float4 b = *reinterpret_cast<const float4*>(inv_s + 4);
-  float2 f;
-  f = act2_to_float2<kBf16>(qz.x);
-  qz.x = float2_to_act2<kBf16>(f.x * (scale * a.x), f.y * (scale * a.y));
-  f = act2_to_float2<kBf16>(qz.y);
-  qz.y = float2_to_act2<kBf16>(f.x * (scale * a.z), f.y * (scale * a.w));
-  f = act2_to_float2<kBf16>(qz.z);
-  qz.z = float2_to_act2<kBf16>(f.x * (scale * b.x), f.y * (scale * b.y));
-  f = act2_to_float2<kBf16>(qz.w);
-  qz.w = float2_to_act2<kBf16>(f.x * (scale * b.z), f.y * (scale * b.w));
-  return qz;
-}
-template <bool kBf16>
-__device__ __forceinline__ uint4 dequant_word_inv(uint32_t w, __half2 bias_lo, __half2 bias_hi,
-                                                  uint32_t bias, float scale,
-                                                  const float* inv_s) {
-  uint4 qz;
-  if constexpr (kBf16) {
-    qz = make_uint4(lop3_and_or(w, 0x000F000Fu, 0x43004300u),
-                    lop3_and_or(w >> 4, 0x000F000Fu, 0x43004300u),
-                    lop3_and_or(w >> 8, 0x000F000Fu, 0x43004300u),
-                    lop3_and_or(w >> 12, 0x000F000Fu, 0x43004300u));
-    qz.x = b2_as_u32(__hsub2(u32_as_b2(qz.x), u32_as_b2(bias)));
-    qz.y = b2_as_u32(__hsub2(u32_as_b2(qz.y), u32_as_b2(bias)));
-    qz.z = b2_as_u32(__hsub2(u32_as_b2(qz.z), u32_as_b2(bias)));
-    qz.w = b2_as_u32(__hsub2(u32_as_b2(qz.w), u32_as_b2(bias)));
-  } else {
-    const __half2 sixteenth = __float2half2_rn(0.0625f);
-    const uint32_t w8 = w >> 8;
-    qz.x = h2_as_u32(__hsub2(u32_as_h2(lop3_and_or(w, 0x000F000Fu, 0x64006400u)), bias_lo));
-    qz.y = h2_as_u32(__hfma2(u32_as_h2(lop3_and_or(w, 0x00F000F0u, 0x64006400u)), sixteenth, bias_hi));
-    qz.z = h2_as_u32(__hsub2(u32_as_h2(lop3_and_or(w8, 0x000F000Fu, 0x64006400u)), bias_lo));
-    qz.w = h2_as_u32(__hfma2(u32_as_h2(lop3_and_or(w8, 0x00F000F0u, 0x64006400u)), sixteenth, bias_hi));
-  }
-  return scale_inv8<kBf16>(qz, scale, inv_s);
-}
-
 // Byte offset of 16-byte chunk c (k = 8c..8c+7) of row r in a 64-wide fp16 tile stored in
 // the 128-byte swizzled K-major layout (8-row atoms of 1024 bytes).
 __device__ __forceinline__ uint32_t sw128_offset(int r, int c) {
@@ -460,9 +322,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   static_assert(kEpi != Epi::kGramDot || kA == ASrc::kGram, "the Gram-form loss");
   static_assert(kEpi != Epi::kSiluMul || kA == ASrc::kPair16,
                 "the SiLU epilogue combines the gate and up accumulators");
-  static_assert((kEpi != Epi::kStoreY && kEpi != Epi::kFused) || kPacked,
-                "fp16 Y comes from the packed sources");
-  static_assert(!kGrp || kEpi == Epi::kFused || kEpi == Epi::kSiluMul, "grouped epilogues");
+  static_assert(kEpi != Epi::kStoreY || kPacked, "fp16 Y comes from the packed sources");
+  static_assert(!kGrp || kEpi == Epi::kSiluMul, "the gated products have a grouped form");
   static_assert(L::kSmem <= kTcSmemMax, "shared memory layout too large");
 
   uint64_t* pempty = pfull + P;
@@ -520,7 +381,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
   if constexpr (kGrp) {
-    if (warp == 0) build_group_table(*tab, args, BN);
+    if (warp == 0) build_group_table(tab->off, tab->tile, args.offsets, args.E, args.M, BN);
     __syncthreads();
     units = static_cast<int64_t>(args.row_tiles) * tab->tile[args.E] * args.k_splits;
   }
@@ -645,9 +506,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (!args.sz_tma) {   // ragged N: this row's zero point and scale from global
             const int64_t g = kb >> 1;
             if (n < N && AWQ_IN_BOUNDS(g < args.K / kGroup)) {
-              const int64_t ge = g + (kGrp ? tu.e * (args.K / kGroup) : 0);
-              z = args.zeros[ge * N + n];
-              sv = args.scales[ge * N + n];
+              z = args.zeros[g * N + n];
+              sv = args.scales[g * N + n];
             }
           }
           // the group's two 64-k blocks: one stage (kBlk = 2) or the two stages s and s1. A
@@ -695,14 +555,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 const int k0 = e * kTcBK + 32 * h + 8 * q;   // k inside the group
-                uint4 o;
-                if (kEpi == Epi::kFused && inv_g != nullptr) {
-                  o = dequant_word_inv<kBf16>(words[q], lo, hi, bias, scf, inv_g + k0);
-                } else {
-                  const uint4 c4 = pair_scales<kBf16>(scf, sc, inv_g, k0);
-                  o = kBf16 ? dequant_word_scaled_bf16(words[q], bias, c4)
-                            : dequant_word_scaled(words[q], lo, hi, c4);
-                }
+                const uint4 c4 = pair_scales<kBf16>(scf, sc, inv_g, k0);
+                const uint4 o = kBf16 ? dequant_word_scaled_bf16(words[q], bias, c4)
+                                      : dequant_word_scaled(words[q], lo, hi, c4);
                 *reinterpret_cast<uint4*>(atile + sw128_offset(r, 4 * h + q)) = o;
               }
             } else {
@@ -711,17 +566,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const uint32_t w0 = pw[0], w1 = pw[1], w2 = pw[2];
               uint4 o, c4;
 #define AWQ_DQ3_CHUNK(I)                                                                    \
-  if (kEpi == Epi::kFused && inv_g != nullptr) {                                           \
-    o = make_uint4(raw3_qz<I, 0, kBf16>(w0, w1, w2, bias), raw3_qz<I, 1, kBf16>(w0, w1, w2, bias), \
-                   raw3_qz<I, 2, kBf16>(w0, w1, w2, bias), raw3_qz<I, 3, kBf16>(w0, w1, w2, bias)); \
-    o = scale_inv8<kBf16>(o, scf, inv_g + e * kTcBK + 32 * h + 8 * (I));                  \
-  } else {                                                                                 \
-    c4 = pair_scales<kBf16>(scf, sc, inv_g, e * kTcBK + 32 * h + 8 * (I));                \
-    o.x = dequant3_pair<I, 0, kBf16>(w0, w1, w2, bias, c4.x);                              \
-    o.y = dequant3_pair<I, 1, kBf16>(w0, w1, w2, bias, c4.y);                              \
-    o.z = dequant3_pair<I, 2, kBf16>(w0, w1, w2, bias, c4.z);                              \
-    o.w = dequant3_pair<I, 3, kBf16>(w0, w1, w2, bias, c4.w);                              \
-  }                                                                                        \
+  c4 = pair_scales<kBf16>(scf, sc, inv_g, e * kTcBK + 32 * h + 8 * (I));                  \
+  o.x = dequant3_pair<I, 0, kBf16>(w0, w1, w2, bias, c4.x);                                \
+  o.y = dequant3_pair<I, 1, kBf16>(w0, w1, w2, bias, c4.y);                                \
+  o.z = dequant3_pair<I, 2, kBf16>(w0, w1, w2, bias, c4.z);                                \
+  o.w = dequant3_pair<I, 3, kBf16>(w0, w1, w2, bias, c4.w);                                \
   *reinterpret_cast<uint4*>(atile + sw128_offset(r, 4 * h + I)) = o;
               AWQ_DQ3_CHUNK(0)
               AWQ_DQ3_CHUNK(1)
@@ -762,8 +611,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int64_t m_end = t.m_end;
       // the columns the MMA wrote
       const int cols = kGrp && m_end - m0 < BN ? static_cast<int>(m_end - m0) : BN;
-      const float bias = kEpi == Epi::kFused && arow < args.N ? fused_bias<kBf16>(args, t.e, arow)
-                                                               : 0.0f;
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * wq) << 16) +
                              static_cast<uint32_t>(buf * L::kAParts * BN);
       const bool unit_ok =
@@ -793,23 +640,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               for (int j = 0; j < 16; ++j) {
                 const int64_t m = m0 + col + j;
                 if (m < args.M) P[m * args.N + arow] = __uint_as_float(v[j]);
-              }
-            }
-          }
-        } else if (kEpi == Epi::kFused) {
-          if (arow < args.N && unit_ok) {
-            if (args.k_splits == 1) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int64_t m = m0 + col + j;
-                if (m < m_end) fused_store<kBf16>(args, m, arow, __uint_as_float(v[j]) + bias);
-              }
-            } else {
-              float* P = args.partial + static_cast<int64_t>(t.ksplit) * args.M * args.N;
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int64_t m = m0 + col + j;
-                if (m < m_end) P[m * args.N + arow] = __uint_as_float(v[j]);
               }
             }
           }
@@ -894,10 +724,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bool ok = true;
       for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
         const TcUnit t = unit_of<BN, kGrp>(u, args, tab, expert);
-        const int32_t row0 = t.row_tile * kTcBM;               // row of the expert's weight
-        const int32_t a_row0 = row0 + (kGrp ? static_cast<int32_t>(t.e * args.N) : 0);
-        const int32_t g_row0 = kGrp ? static_cast<int32_t>(t.e * (args.K / kGroup)) : 0;
-        const float* inv_e = args.inv_s + (kGrp ? t.e * args.K : 0);   // read only with inv_s
+        const int32_t row0 = t.row_tile * kTcBM;
         // a last slot that runs past the unit's K slice loads groups it does not use (zero
         // filled past K); the transaction count is always the full box
         for (int i = 0; i < t.nkb; i += 2 * L::kPG) {
@@ -915,14 +742,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           mbar_arrive_expect_tx(&pfull[ps],
                                 L::kPBytes + (args.sz_tma ? L::kSZBytes : 0) + inv_bytes);
           tma_load_2d(smem + L::kPOff + ps * L::kPBytes, &tmap_a, &pfull[ps],
-                      g * (L::kPGroupBytes / 4), a_row0);
+                      g * (L::kPGroupBytes / 4), row0);
           if (inv_bytes != 0 && AWQ_IN_BOUNDS(g < G && inv_bytes <= L::kInvBytes))
-            bulk_load_1d(smem + L::kIOff + ps * L::kInvBytes, inv_e + g * kGroup, inv_bytes,
+            bulk_load_1d(smem + L::kIOff + ps * L::kInvBytes, args.inv_s + g * kGroup, inv_bytes,
                          &pfull[ps]);
           if (args.sz_tma) {
             uint8_t* sz = smem + L::kSZOff + ps * L::kSZBytes;
-            tma_load_2d(sz, &tmap_s, &pfull[ps], row0, g_row0 + g);
-            tma_load_2d(sz + L::kPG * kTcBM * 2, &tmap_z, &pfull[ps], row0, g_row0 + g);
+            tma_load_2d(sz, &tmap_s, &pfull[ps], row0, g);
+            tma_load_2d(sz + L::kPG * kTcBM * 2, &tmap_z, &pfull[ps], row0, g);
           }
           if (++ps == P) { ps = 0; pph ^= 1; }
         }
@@ -939,16 +766,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // The fused epilogue on the sum over the K slices of the fp32 partial sums, slices added in
-// order. One thread per output; rows no expert has are left as they are.
+// order. One thread per output of one packed weight.
 template <bool kBf16>
 __global__ void splitk_fused_kernel(const TcArgs args) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const int64_t MN = args.M * args.N;
   if (i >= MN) return;
-  const int64_t m = i / args.N, n = i % args.N;
+  const int64_t n = i % args.N;
   float acc = args.partial[i];
   for (int s = 1; s < args.k_splits; ++s) acc += args.partial[s * MN + i];
-  fused_store<kBf16>(args, m, n, acc + fused_bias<kBf16>(args, 0, n));
+  fused_store<kBf16>(args.epi, static_cast<act_t<kBf16>*>(args.Y), i,
+                     acc + fused_bias<kBf16>(args.epi, n));
 }
 
 // Y[m, n] = fp16 (bf16) of the sum over the K slices of the fp32 partial sums, slices added

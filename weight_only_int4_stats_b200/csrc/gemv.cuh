@@ -19,6 +19,7 @@
 // The 8 warps' partial sums are added in a fixed order through shared memory.
 #pragma once
 #include "common.cuh"
+#include "fused.cuh"
 
 namespace awq {
 
@@ -345,12 +346,14 @@ __device__ __forceinline__ void dequant_word_qz_bf16(uint32_t w, uint32_t bias, 
   for (int i = 0; i < 4; ++i) out[i] = b2_as_u32(__hsub2(u32_as_b2(out[i]), u32_as_b2(bias)));
 }
 
-template <int kNTiles, bool kOffset, bool kBf16 = false, int kBits = 4>
+// kFused: Y goes through the fused epilogue (bias, activation, product, sum) as it is stored.
+template <int kNTiles, bool kOffset, bool kBf16 = false, int kBits = 4, bool kFused = false>
 __global__ void __launch_bounds__(kG4Threads, 2) gemv_stream_kernel(
     const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_s,
     const __grid_constant__ CUtensorMap tmap_z,
     const act_t<kBf16>* __restrict__ X, int M, int64_t N, int64_t K,
-    const float* __restrict__ inv_s, act_t<kBf16>* __restrict__ Y, G4Smem lay, unsigned flags) {
+    const float* __restrict__ inv_s, act_t<kBf16>* Y, G4Smem lay, unsigned flags,
+    const FusedEpi epi) {
   static_assert(kBits == 4 || kBits == 3, "4- or 3-bit codes");
   constexpr int kTok = 8 * kNTiles;
   constexpr int kRowW = kG4KC * kBits / 32;            // packed words of one row in a unit
@@ -545,6 +548,11 @@ __global__ void __launch_bounds__(kG4Threads, 2) gemv_stream_kernel(
   uint32_t ph = 0;
   int64_t tile = t0;
   for (int64_t u = 0; u < units; ++u) {
+    // what the epilogue reads of this lane's outputs travels while the tile's last unit is
+    // awaited and computed
+    FusedIn<kBf16> fin;
+    if (kFused && chunk == C - 1 && warp < kNTiles)
+      fin.load(epi, tile * kGemvRows + rw, 8 * warp + 2 * c, N, M);
     ok = __all_sync(0xffffffffu, ok && mbar_wait(&full[slot], ph));
     if (threadIdx.x == 0 && u < kTrMaxUnits) AWQ_TRACE_AT(rec, kTrUnit0 + u, globaltimer_ns());
     // Copy this warp's operands of the unit (its two groups: packed codes of rows r and r + 8,
@@ -695,6 +703,10 @@ __global__ void __launch_bounds__(kG4Threads, 2) gemv_stream_kernel(
         }
         const int64_t nA = tile * kGemvRows + rw, nB = nA + 8;
         const int m0 = 8 * t + 2 * c, m1 = m0 + 1;
+        if constexpr (kFused) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = fin.apply(epi, v[i], i);
+        }
         if (nA < N && AWQ_IN_BOUNDS(tile < t1)) {
           if (m0 < M) Y[static_cast<int64_t>(m0) * N + nA] = float_to_act<kBf16>(v[0]);
           if (m1 < M) Y[static_cast<int64_t>(m1) * N + nA] = float_to_act<kBf16>(v[1]);
