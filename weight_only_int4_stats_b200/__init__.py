@@ -8,6 +8,7 @@ no fallback: if the library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -283,17 +284,22 @@ def awq_silu_mul_gemm(X: torch.Tensor, W_gate: torch.Tensor, W_up: torch.Tensor,
 
 
 # ------------------------------------------------------------------ fused epilogue, experts
+# the current stream's handle without making a Stream object for it (3 us a call)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}   # AWQ_ACT_*
 
 
-def _arg(t, dtype, shape, device, name):
-    """The address of a contiguous CUDA tensor of this dtype, shape and device (None: NULL)."""
+def _arg(t, dtype, shape, index, name):
+    """The address of a contiguous tensor of this dtype and shape on CUDA device `index` (None:
+    NULL)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
         raise TypeError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} "
-                        f"on {device}, got {t.dtype} {tuple(t.shape)} on {t.device} "
-                        f"(contiguous={t.is_contiguous()})")
+                        f"on {'cuda:%d' % index if index >= 0 else 'a CUDA device'}, got {t.dtype} "
+                        f"{tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
     return t.data_ptr()
 
 
@@ -313,35 +319,42 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _call(fn, device, stream, need, workspace, args):
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(L, fn, *sizes):
+    return getattr(L, fn)(*sizes)
+
+
+def _call(fn, index, stream, need, workspace, args):
     """Calls the C entry point `fn` with `args`, then (workspace, its bytes) unless need is
     None, then the stream; on the inputs' device, with scratch memory that belongs to the
     stream that uses it."""
-    if not device.type == "cuda":
-        raise TypeError(f"{fn}: expected CUDA tensors, got {device}")
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _call(fn, device, stream, need, workspace, args)
-    s = torch.cuda.current_stream() if stream is None else stream
+    if index < 0:
+        raise TypeError(f"{fn}: expected CUDA tensors")
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _call(fn, index, stream, need, workspace, args)
     if need is not None:
         ws = workspace
         if ws is None and need > 0:
-            ws = _new(need, torch.uint8, device, stream)
+            ws = _new(need, torch.uint8, torch.device("cuda", index), stream)
         if ws is None:
             args += (None, 0)
         else:
-            if ws.device != device or not ws.is_contiguous():
-                raise TypeError(f"workspace: expected a contiguous tensor on {device}")
+            if ws.get_device() != index or not ws.is_contiguous():
+                raise TypeError(f"workspace: expected a contiguous tensor on cuda:{index}")
             args += (ws.data_ptr(), ws.numel() * ws.element_size())
-    _check(fn, getattr(lib(), fn)(*args, s.cuda_stream))
+    s = _current_raw_stream(index) if stream is None else stream.cuda_stream
+    code = getattr(lib(), fn)(*args, s)
+    if code != 0:
+        raise AwqError(fn, code)
 
 
-def _activations(X, K):
-    if X.dtype not in (torch.float16, torch.bfloat16):
+def _activations(X, K, index):
+    if X.dtype is not torch.float16 and X.dtype is not torch.bfloat16:
         raise TypeError(f"X: expected torch.float16 or torch.bfloat16, got {X.dtype}")
     if X.dim() != 2:
         raise TypeError(f"X: expected a 2-d tensor, got shape {tuple(X.shape)}")
-    return _arg(X, X.dtype, (X.shape[0], K), X.device, "X")
+    return _arg(X, X.dtype, (X.shape[0], K), index, "X")
 
 
 def awq_gemm_w4a16_epilogue(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
@@ -358,18 +371,18 @@ def awq_gemm_w4a16_epilogue(X: torch.Tensor, qweight: torch.Tensor, scales: torc
     X fp16 or bf16 [M, K]; bias [N], mul and residual [M, N] in X's dtype, each optional; act a
     key of ACTIVATIONS. ``out`` may be ``mul`` or ``residual`` itself. ``weights_ready`` as for
     awq_gemm_w4a16."""
-    dev, t = X.device, X.dtype
-    x, M = _activations(X, K), X.shape[0]
-    Y = _new((M, N), t, dev, stream) if out is None else out
+    dev, t, M = X.get_device(), X.dtype, X.shape[0]
+    x, G = _activations(X, K, dev), K // GROUP
+    Y = _new((M, N), t, X.device, stream) if out is None else out
     _call("awq_gemm_w4a16_epilogue", dev, stream,
-          lib().awq_gemm_epilogue_workspace_size(M, N, K, bits), workspace,
+          _workspace_bytes(lib(), "awq_gemm_epilogue_workspace_size", M, N, K, bits), workspace,
           (x, M, _arg(qweight, torch.int32, (N, packed_words_per_row(K, bits)), dev, "qweight"),
-           _arg(scales, torch.float16, (K // GROUP, N), dev, "scales"),
-           _arg(zeros, torch.uint8, (K // GROUP, N), dev, "zeros"), N, K, bits, group,
+           _arg(scales, torch.float16, (G, N), dev, "scales"),
+           _arg(zeros, torch.uint8, (G, N), dev, "zeros"), N, K, bits, group,
            _arg(inv_s, torch.float32, (K,), dev, "inv_s"), _arg(bias, t, (N,), dev, "bias"),
            _act(act), _arg(mul, t, (M, N), dev, "mul"),
            _arg(residual, t, (M, N), dev, "residual"),
-           (WEIGHTS_READY if weights_ready else 0) | (BF16 if t == torch.bfloat16 else 0),
+           (WEIGHTS_READY if weights_ready else 0) | (BF16 if t is torch.bfloat16 else 0),
            _arg(Y, t, (M, N), dev, "out")))
     return Y
 
@@ -389,19 +402,19 @@ def awq_gemm_w4a16_grouped(X: torch.Tensor, offsets: torch.Tensor, qweight: torc
     qweight [E, N, words], scales and zeros [E, K // 128, N], inv_s [E, K], bias [E, N]; mul,
     residual and the result [T, N]. Rows of no expert are left as they were in ``out``
     (undefined without it)."""
-    dev, t = X.device, X.dtype
-    x, T, E = _activations(X, K), X.shape[0], offsets.numel() - 1
-    Y = _new((T, N), t, dev, stream) if out is None else out
+    dev, t, T, E = X.get_device(), X.dtype, X.shape[0], offsets.numel() - 1
+    x, G = _activations(X, K, dev), K // GROUP
+    Y = _new((T, N), t, X.device, stream) if out is None else out
     _call("awq_gemm_w4a16_grouped", dev, stream,
-          lib().awq_gemm_grouped_workspace_size(T, E, N, K, bits), workspace,
+          _workspace_bytes(lib(), "awq_gemm_grouped_workspace_size", T, E, N, K, bits), workspace,
           (x, T, _arg(offsets, torch.int32, (E + 1,), dev, "offsets"), E,
            _arg(qweight, torch.int32, (E, N, packed_words_per_row(K, bits)), dev, "qweight"),
-           _arg(scales, torch.float16, (E, K // GROUP, N), dev, "scales"),
-           _arg(zeros, torch.uint8, (E, K // GROUP, N), dev, "zeros"), N, K, bits, group,
+           _arg(scales, torch.float16, (E, G, N), dev, "scales"),
+           _arg(zeros, torch.uint8, (E, G, N), dev, "zeros"), N, K, bits, group,
            _arg(inv_s, torch.float32, (E, K), dev, "inv_s"),
            _arg(bias, t, (E, N), dev, "bias"), _act(act), _arg(mul, t, (T, N), dev, "mul"),
            _arg(residual, t, (T, N), dev, "residual"),
-           (WEIGHTS_READY if weights_ready else 0) | (BF16 if t == torch.bfloat16 else 0),
+           (WEIGHTS_READY if weights_ready else 0) | (BF16 if t is torch.bfloat16 else 0),
            _arg(Y, t, (T, N), dev, "out")))
     return Y
 
@@ -412,10 +425,10 @@ def awq_act_stats_grouped(X: torch.Tensor, offsets: torch.Tensor,
     """s_x[e, k] = mean |X[row, k]| over expert e's rows offsets[e] .. offsets[e + 1] - 1 (fp32
     [E, K]; 0 for an expert without rows), for fp16 X [T, K] sorted by expert and int32 offsets
     [E + 1] on the GPU."""
-    dev, (T, K), E = X.device, X.shape, offsets.numel() - 1
-    s_x = _new((E, K), torch.float32, dev, stream) if out is None else out
+    dev, (T, K), E = X.get_device(), X.shape, offsets.numel() - 1
+    s_x = _new((E, K), torch.float32, X.device, stream) if out is None else out
     _call("awq_act_stats_grouped", dev, stream,
-          lib().awq_act_stats_grouped_workspace_size(T, E, K), workspace,
+          _workspace_bytes(lib(), "awq_act_stats_grouped_workspace_size", T, E, K), workspace,
           (_arg(X, torch.float16, (T, K), dev, "X"), T,
            _arg(offsets, torch.int32, (E + 1,), dev, "offsets"), E, K,
            _arg(s_x, torch.float32, (E, K), dev, "out")))
@@ -427,10 +440,9 @@ def awq_silu_mul_gemm_grouped(X: torch.Tensor, offsets: torch.Tensor, W_gate: to
                               stream=None) -> torch.Tensor:
     """H = silu(X W_gate[e]^T) * (X W_up[e]^T) (fp16 [T, I]) for rows sorted by expert: expert
     e's rows of X [T, K] are offsets[e] .. offsets[e + 1] - 1; W_gate, W_up fp16 [E, I, K]."""
-    dev, (T, K) = X.device, X.shape
-    E, I = offsets.numel() - 1, W_gate.shape[1]
-    H = _new((T, I), torch.float16, dev, stream) if out is None else out
-    f16 = torch.float16
+    dev, (T, K) = X.get_device(), X.shape
+    E, I, f16 = offsets.numel() - 1, W_gate.shape[1], torch.float16
+    H = _new((T, I), f16, X.device, stream) if out is None else out
     _call("awq_silu_mul_gemm_grouped", dev, stream, None, None,
           (_arg(X, f16, (T, K), dev, "X"), T,
            _arg(offsets, torch.int32, (E + 1,), dev, "offsets"), E,

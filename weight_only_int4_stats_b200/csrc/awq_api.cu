@@ -871,6 +871,8 @@ awq_status launch_pdl(void (*kern)(KArgs...), dim3 grid, int threads, int smem, 
 struct FusedPlan {
   enum Kind { kDecode, kStream, kTensor } kind;
   int rb, xrows, slots;   // kStream
+  int splits;             // kTensor: K slices, and where their partial sums start
+  size_t prepared;
   size_t workspace;
 };
 
@@ -898,7 +900,7 @@ awq_status launch_stream(const FusedPlan& plan, const void* X, const float* inv_
     return AWQ_ERR_CUDA;
   // X in the kernel's layout first, in the workspace
   const awq_status r = launch_pdl(
-      awq::prepare_rows_kernel<kBf16>, dim3(static_cast<unsigned>(a.T)), awq::kPrepThreads, 0, st,
+      awq::prepare_rows_kernel<kBf16, true>, dim3(static_cast<unsigned>(a.T)), awq::kPrepThreads, 0, st,
       static_cast<const uint4*>(X), a.T, a.K, inv_s, a.offsets, a.E, L::kChunkG, L::kXChunk,
       static_cast<uint8_t*>(workspace));
   if (r != AWQ_OK) return r;
@@ -963,19 +965,22 @@ FusedPlan fused_plan(int64_t T, int64_t E, int64_t N, int64_t K, bool grouped) {
     return p;
   }
   p.kind = FusedPlan::kTensor;
-  const int splits = grouped ? 1 : splitk_for(T, N, K);
-  p.workspace = splits > 1 ? align256(static_cast<size_t>(splits) * T * N * sizeof(float)) : 0;
+  // prepared activations (bf16) and their factors, then the partial sums of K slices
+  p.prepared = align256(static_cast<size_t>(T) * (2 * K + sizeof(float)));
+  p.splits = grouped ? 1 : splitk_for(T, N, K);
+  p.workspace = p.prepared +
+                (p.splits > 1 ? align256(static_cast<size_t>(p.splits) * T * N * sizeof(float)) : 0);
   return p;
 }
 
-template <int BN, bool kBf16, int kBits>
+template <int BN, bool kBf16, int kBits, bool kInv>
 awq_status launch_tensor_bn(const void* X, const uint32_t* qweight, awq::TcArgs a, int early,
-                            cudaStream_t st) {
+                            cudaStream_t st) {   // X fp16, whatever Y's type
   using L = awq::TfLayout<BN, kBits>;
   static std::atomic<bool> attr_set[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return AWQ_ERR_CUDA;
-  auto kern = awq::tc_fused_kernel<BN, kBf16, kBits>;
+  auto kern = awq::tc_fused_kernel<BN, kBf16, kBits, kInv>;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem) !=
         cudaSuccess)
@@ -983,9 +988,7 @@ awq_status launch_tensor_bn(const void* X, const uint32_t* qweight, awq::TcArgs 
     attr_set[dev].store(true, std::memory_order_release);
   }
   CUtensorMap tx, tw;
-  if (!make_tmap_2d(&tx, X, kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                    2, a.M, a.K, BN, awq::kTcBK, true) ||
+  if (!make_tmap_2d(&tx, X, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.M, a.K, BN, awq::kTcBK, true) ||
       !make_tmap_2d(&tw, qweight, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.E * a.N, a.K * kBits / 32,
                     awq::kTcBM, L::kRowBytes / 4, kBits == 4))
     return AWQ_ERR_CUDA;
@@ -1004,14 +1007,14 @@ int tensor_bn(int64_t T, int64_t E) {
   return mean <= 32 ? 32 : mean <= 64 ? 64 : mean <= 128 ? 128 : 192;
 }
 
-template <bool kBf16, int kBits>
+template <bool kBf16, int kBits, bool kInv = false>
 awq_status launch_tensor(const void* X, const uint32_t* qweight, const awq::TcArgs& a, int early,
                          cudaStream_t st) {
   switch (tensor_bn(a.M, a.E)) {
-    case 32: return launch_tensor_bn<32, kBf16, kBits>(X, qweight, a, early, st);
-    case 64: return launch_tensor_bn<64, kBf16, kBits>(X, qweight, a, early, st);
-    case 128: return launch_tensor_bn<128, kBf16, kBits>(X, qweight, a, early, st);
-    default: return launch_tensor_bn<192, kBf16, kBits>(X, qweight, a, early, st);
+    case 32: return launch_tensor_bn<32, kBf16, kBits, kInv>(X, qweight, a, early, st);
+    case 64: return launch_tensor_bn<64, kBf16, kBits, kInv>(X, qweight, a, early, st);
+    case 128: return launch_tensor_bn<128, kBf16, kBits, kInv>(X, qweight, a, early, st);
+    default: return launch_tensor_bn<192, kBf16, kBits, kInv>(X, qweight, a, early, st);
   }
 }
 
@@ -1062,7 +1065,6 @@ awq_status fused_gemm(const void* X, int64_t T, const int32_t* offsets, int64_t 
     return bits == 3 ? launch_stream_plan<false, 3>(plan, X, inv_s, qweight, a, workspace, st)
                      : launch_stream_plan<false, 4>(plan, X, inv_s, qweight, a, workspace, st);
   }
-  const int splits = offsets == nullptr ? splitk_for(T, N, K) : 1;
   awq::TcArgs args{};
   args.M = T;
   args.N = N;
@@ -1071,21 +1073,35 @@ awq_status fused_gemm(const void* X, int64_t T, const int32_t* offsets, int64_t 
   args.scales = reinterpret_cast<const __half*>(scales);
   args.zeros = zeros;
   args.Y = Y;
-  args.k_splits = splits;
-  args.partial = splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  args.k_splits = plan.splits;
+  args.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.prepared);
   args.inv_s = inv_s;
   args.offsets = offsets;
   args.E = static_cast<int>(E);
   args.epi = epi;
   awq_status r;
-  const int early = offsets == nullptr && (flags & AWQ_GEMM_WEIGHTS_READY) != 0;
+  // (behind the preparation the weights of any call are there: see the kernel)
+  int early = offsets == nullptr && (flags & AWQ_GEMM_WEIGHTS_READY) != 0;
+  if (bf16) {
+    r = launch_pdl(awq::prepare_rows_kernel<true, false>, dim3(static_cast<unsigned>(T)),
+                   awq::kPrepThreads, 0, st, static_cast<const uint4*>(X), static_cast<int>(T), K,
+                   inv_s, offsets, static_cast<int>(E), 1, 0, static_cast<uint8_t*>(workspace));
+    if (r != AWQ_OK) return r;
+    X = workspace;
+    args.factors = reinterpret_cast<const float*>(static_cast<uint8_t*>(workspace) + T * K * 2);
+    args.inv_s = nullptr;
+    early = 1;
+  }
   if (bf16)
     r = bits == 3 ? launch_tensor<true, 3>(X, qweight, args, early, st)
                   : launch_tensor<true, 4>(X, qweight, args, early, st);
+  else if (inv_s != nullptr)
+    r = bits == 3 ? launch_tensor<false, 3, true>(X, qweight, args, early, st)
+                  : launch_tensor<false, 4, true>(X, qweight, args, early, st);
   else
     r = bits == 3 ? launch_tensor<false, 3>(X, qweight, args, early, st)
                   : launch_tensor<false, 4>(X, qweight, args, early, st);
-  if (r != AWQ_OK || splits == 1) return r;
+  if (r != AWQ_OK || plan.splits == 1) return r;
   const unsigned grid = static_cast<unsigned>((T * N + 255) / 256);
   if (bf16) awq::splitk_fused_kernel<true><<<grid, 256, 0, st>>>(args);
   else awq::splitk_fused_kernel<false><<<grid, 256, 0, st>>>(args);

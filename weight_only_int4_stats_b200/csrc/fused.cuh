@@ -18,14 +18,16 @@ struct FusedEpi {
   int act;                // Act
 };
 
-// act(v) in fp32. A NaN stays one (with relu too); silu and gelu as their formulas give it.
+// act(v) in fp32. A NaN stays one (with relu too); silu and gelu as their formulas give it, the
+// tanh form by (1 + tanh u) / 2 = 1 / (1 + exp(-2u)). The fast exponential and division are within
+// a few fp32 roundings, and far out v / inf is the limit 0.
 __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
     case kActRelu: return v < 0.0f ? 0.0f : v;
-    case kActSilu: return __fdiv_rn(v, 1.0f + expf(-v));
+    case kActSilu: return __fdividef(v, 1.0f + __expf(-v));
     case kActGelu: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-    case kActGeluTanh:   // sqrt(2 / pi) (v + 0.044715 v^3)
-      return 0.5f * v * (1.0f + tanhf(0.79788456080286536f * fmaf(0.044715f * v * v, v, v)));
+    case kActGeluTanh:   // 2 u = 2 sqrt(2 / pi) (v + 0.044715 v^3)
+      return __fdividef(v, 1.0f + __expf(-1.5957691216057308f * fmaf(0.044715f * v * v, v, v)));
     default: return v;
   }
 }

@@ -19,11 +19,17 @@
 //                warp % 4); the sets take the K blocks in turn, so that four chains of
 //                shared-memory reads, arithmetic, TMEM stores and barriers run at once
 //   warps 20..27 epilogue: two warps per quarter, each half of the token columns
-// A K block, the unit of the X and A pipelines, is 128 k (a group), or 64 k with BN = 192. TMEM:
-// two accumulators of BN columns and kNA A stages. BN stops at 192 so that both accumulators fit
-// beside four A stages and a tile's epilogue always overlaps the next tile's products. (A set's
-// turn comes round after four blocks, and a barrier's parity tells only neighbouring phases
-// apart: a stage must not come round sooner, so kNA >= the sets.)
+// X comes in blocks of 128 k (a group). A stages hold a group too, or half of one with BN = 192.
+// TMEM: two accumulators of BN columns and kNA A stages. BN stops at 192 so that both accumulators
+// fit beside four A stages and a tile's epilogue always overlaps the next tile's products. (A
+// set's turn comes round after four A stages, and a barrier's parity tells only neighbouring
+// phases apart: a stage must not come round sooner, so kNA >= the sets.)
+// Waiting on a barrier whose phase is already complete still takes about 100 cycles, so the waits
+// of one step are polled together, and the MMA issuer takes a whole group a step.
+// The products are fp16: bf16 activations come from prepare_rows_kernel as fp16, scaled by a power
+// of two per row (with inv_s already in), and the epilogue takes the row's factor off. bf16
+// weights would need (q - z) * scale in two bf16 parts to be rounded only once (19 operations a
+// word of 8 codes, 45 with inv_s, against 13), and the dequantization is what bounds this kernel.
 // Packed codes: 4 bits: boxes of 128 rows x 128 bytes (two groups) with the 128-byte swizzle;
 // 3 bits: one box of 3 or 5 groups (an odd multiple of 48 bytes per row, so that the 16-byte
 // reads of eight consecutive rows fall into eight different bank groups as they are).
@@ -31,6 +37,7 @@
 #include "common.cuh"
 #include "fused.cuh"
 #include "gemm_tc.cuh"
+#include "prepare.cuh"
 
 namespace awq {
 
@@ -42,10 +49,10 @@ constexpr int kTfThreads = (kTfEpiWarp0 + 8) * 32;
 template <int BN, int kBits>
 struct TfLayout {
   static_assert(BN == 32 || BN == 64 || BN == 128 || BN == 192, "token tiles");
-  static constexpr int kHB = BN == 192 ? 1 : 2;                   // 64-k halves of a K block
-  static constexpr int kXHalf = BN * kTcBK * 2;
-  static constexpr int kXBytes = kHB * kXHalf;                    // a K block of X
-  static constexpr int kXStages = BN == 192 ? 5 : BN == 128 ? 3 : BN == 64 ? 4 : 6;
+  static constexpr int kXHalf = BN * kTcBK * 2;                   // 64 k of X
+  static constexpr int kXBytes = 2 * kXHalf;
+  static constexpr int kXStages = BN >= 128 ? 3 : BN == 64 ? 4 : 6;
+  static constexpr int kHB = BN == 192 ? 1 : 2;                   // 64-k halves of an A stage
   static constexpr int kACols = kHB * 32;                         // TMEM columns of an A stage
   static constexpr int kNA = BN >= 128 ? 4 : 6;
   static constexpr int kAccCol = 0;
@@ -79,6 +86,18 @@ __device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, 
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// mbar_wait on two or three barriers at once: their polls are in flight together.
+__device__ __forceinline__ bool mbar_wait_all(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1) {
+  const bool r0 = mbar_try_wait(smem_u32(b0), p0), r1 = mbar_try_wait(smem_u32(b1), p1);
+  return (r0 || mbar_wait(b0, p0)) && (r1 || mbar_wait(b1, p1));
+}
+__device__ __forceinline__ bool mbar_wait_all(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1,
+                                              uint64_t* b2, uint32_t p2) {
+  const bool r0 = mbar_try_wait(smem_u32(b0), p0), r1 = mbar_try_wait(smem_u32(b1), p1),
+             r2 = mbar_try_wait(smem_u32(b2), p2);
+  return (r0 || mbar_wait(b0, p0)) && (r1 || mbar_wait(b1, p1)) && (r2 || mbar_wait(b2, p2));
 }
 
 // mbar_wait for a warp that has time: it looks only now and then, so that its polling takes no
@@ -160,60 +179,65 @@ __device__ __forceinline__ TfUnit tf_unit(unsigned u, const TcArgs& a, const Gro
   return t;
 }
 
+// Two fp32 products in one instruction.
+__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(static_cast<uint64_t>(__float_as_uint(a.y)) << 32 | __float_as_uint(a.x)),
+        "l"(static_cast<uint64_t>(__float_as_uint(b.y)) << 32 | __float_as_uint(b.x)));
+  return make_float2(__uint_as_float(static_cast<uint32_t>(d)),
+                     __uint_as_float(static_cast<uint32_t>(d >> 32)));
+}
+
 // 32 weights (one 32-k quarter of a group: 4 words at 4 bits, 3 at 3 bits) of a row to 16 MMA
-// operand pairs: exact q - z, then the scale with one rounding to 16 bits. With bf16 the fp16
-// scale goes in as two bf16 parts, (q - z) hi + (q - z) lo, since rounding it to one would add an
-// error of the size of the product's own; inv_s (this quarter's) likewise from fp32.
-template <bool kBf16, int kBits>
-__device__ __forceinline__ void dequant32(const uint32_t* w, uint32_t z, uint32_t sc_hi,
-                                          uint32_t sc_lo, float scf, const float* inv,
-                                          uint32_t (&o)[16]) {
-  const uint32_t bias = ((kBf16 ? 0x4300u : 0x6400u) | z) * 0x00010001u;
+// operand pairs: exact q - z, then the scale with one rounding to fp16; with inv_s (this
+// quarter's) scale * inv_s[k] in fp32 and the product rounded once. (A factor rounded to fp16
+// before the product would make three roundings with the output's, sqrt(3) of one, where this
+// has sqrt(2).)
+template <int kBits, bool kInv>
+__device__ __forceinline__ void dequant32(const uint32_t* w, uint32_t z, uint32_t sc, float scf,
+                                          const float* inv, uint32_t (&o)[16]) {
+  const uint32_t bias = (0x6400u | z) * 0x00010001u;
   if constexpr (kBits == 4) {
     const __half2 hi = u32_as_h2((0xD400u | (z << 4)) * 0x00010001u);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t v[4];
-      if constexpr (kBf16) dequant_word_qz_bf16(w[j], bias, v);
-      else dequant_word_qz(w[j], u32_as_h2(bias), hi, v);
+      dequant_word_qz(w[j], u32_as_h2(bias), hi, v);
 #pragma unroll
       for (int q = 0; q < 4; ++q) o[4 * j + q] = v[q];
     }
   } else {
-    o[0] = raw3_qz<0, 0, kBf16>(w[0], w[1], w[2], bias);
-    o[1] = raw3_qz<0, 1, kBf16>(w[0], w[1], w[2], bias);
-    o[2] = raw3_qz<0, 2, kBf16>(w[0], w[1], w[2], bias);
-    o[3] = raw3_qz<0, 3, kBf16>(w[0], w[1], w[2], bias);
-    o[4] = raw3_qz<1, 0, kBf16>(w[0], w[1], w[2], bias);
-    o[5] = raw3_qz<1, 1, kBf16>(w[0], w[1], w[2], bias);
-    o[6] = raw3_qz<1, 2, kBf16>(w[0], w[1], w[2], bias);
-    o[7] = raw3_qz<1, 3, kBf16>(w[0], w[1], w[2], bias);
-    o[8] = raw3_qz<2, 0, kBf16>(w[0], w[1], w[2], bias);
-    o[9] = raw3_qz<2, 1, kBf16>(w[0], w[1], w[2], bias);
-    o[10] = raw3_qz<2, 2, kBf16>(w[0], w[1], w[2], bias);
-    o[11] = raw3_qz<2, 3, kBf16>(w[0], w[1], w[2], bias);
-    o[12] = raw3_qz<3, 0, kBf16>(w[0], w[1], w[2], bias);
-    o[13] = raw3_qz<3, 1, kBf16>(w[0], w[1], w[2], bias);
-    o[14] = raw3_qz<3, 2, kBf16>(w[0], w[1], w[2], bias);
-    o[15] = raw3_qz<3, 3, kBf16>(w[0], w[1], w[2], bias);
+    o[0] = raw3_qz<0, 0>(w[0], w[1], w[2], bias);
+    o[1] = raw3_qz<0, 1>(w[0], w[1], w[2], bias);
+    o[2] = raw3_qz<0, 2>(w[0], w[1], w[2], bias);
+    o[3] = raw3_qz<0, 3>(w[0], w[1], w[2], bias);
+    o[4] = raw3_qz<1, 0>(w[0], w[1], w[2], bias);
+    o[5] = raw3_qz<1, 1>(w[0], w[1], w[2], bias);
+    o[6] = raw3_qz<1, 2>(w[0], w[1], w[2], bias);
+    o[7] = raw3_qz<1, 3>(w[0], w[1], w[2], bias);
+    o[8] = raw3_qz<2, 0>(w[0], w[1], w[2], bias);
+    o[9] = raw3_qz<2, 1>(w[0], w[1], w[2], bias);
+    o[10] = raw3_qz<2, 2>(w[0], w[1], w[2], bias);
+    o[11] = raw3_qz<2, 3>(w[0], w[1], w[2], bias);
+    o[12] = raw3_qz<3, 0>(w[0], w[1], w[2], bias);
+    o[13] = raw3_qz<3, 1>(w[0], w[1], w[2], bias);
+    o[14] = raw3_qz<3, 2>(w[0], w[1], w[2], bias);
+    o[15] = raw3_qz<3, 3>(w[0], w[1], w[2], bias);
   }
-  if (inv == nullptr) {
+  if constexpr (!kInv) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      if constexpr (kBf16)
-        o[j] = b2_as_u32(__hfma2(u32_as_b2(o[j]), u32_as_b2(sc_hi),
-                                 __hmul2(u32_as_b2(o[j]), u32_as_b2(sc_lo))));
-      else
-        o[j] = h2_as_u32(__hmul2(u32_as_h2(o[j]), u32_as_h2(sc_hi)));
-    }
+    for (int j = 0; j < 16; ++j) o[j] = h2_as_u32(__hmul2(u32_as_h2(o[j]), u32_as_h2(sc)));
   } else {
+    const float2 ss = make_float2(scf, scf);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float4 s = reinterpret_cast<const float4*>(inv)[j];
-      float2 f = act2_to_float2<kBf16>(o[2 * j]);
-      o[2 * j] = float2_to_act2<kBf16>(f.x * (scf * s.x), f.y * (scf * s.y));
-      f = act2_to_float2<kBf16>(o[2 * j + 1]);
-      o[2 * j + 1] = float2_to_act2<kBf16>(f.x * (scf * s.z), f.y * (scf * s.w));
+      float2 f = mul_f32x2(__half22float2(u32_as_h2(o[2 * j])), mul_f32x2(ss, make_float2(s.x, s.y)));
+      o[2 * j] = float2_to_act2<false>(f.x, f.y);
+      f = mul_f32x2(__half22float2(u32_as_h2(o[2 * j + 1])), mul_f32x2(ss, make_float2(s.z, s.w)));
+      o[2 * j + 1] = float2_to_act2<false>(f.x, f.y);
     }
   }
 }
@@ -240,7 +264,8 @@ __device__ __forceinline__ void fused_columns(const FusedEpi& f, act_t<kBf16>* Y
   }
 }
 
-template <int BN, bool kBf16, int kBits>
+// kBf16: the type of Y and the epilogue's operands. kInv: inv_s goes into the weights.
+template <int BN, bool kBf16, int kBits, bool kInv>
 __global__ void __launch_bounds__(kTfThreads, 1)
     tc_fused_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     const __grid_constant__ CUtensorMap tmap_w, const TcArgs args, const int early) {
@@ -310,15 +335,14 @@ __global__ void __launch_bounds__(kTfThreads, 1)
       bool ok = true;
       for (unsigned u = blockIdx.x; u < units && ok; u += gridDim.x) {
         const TfUnit t = tf_unit<BN>(u, args, tab, G);
-        const int blocks = 2 * t.groups / L::kHB;
-        for (int i = 0; i < blocks; ++i) {
+        for (int i = 0; i < t.groups; ++i) {
           ok = mbar_wait(&xempty[s], ph ^ 1);
           if (!ok) break;
           mbar_arrive_expect_tx(&xfull[s], L::kXBytes);
 #pragma unroll
-          for (int h = 0; h < L::kHB; ++h)
+          for (int h = 0; h < 2; ++h)
             tma_load_2d(smem + s * L::kXBytes + h * L::kXHalf, &tmap_x, &xfull[s],
-                        (2 * t.g0 + i * L::kHB + h) * kTcBK, t.m0);
+                        (2 * (t.g0 + i) + h) * kTcBK, t.m0);
           if (++s == NX) { s = 0; ph ^= 1; }
         }
       }
@@ -333,30 +357,38 @@ __global__ void __launch_bounds__(kTfThreads, 1)
     bool ok = true;
     for (unsigned u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const TfUnit t = tf_unit<BN>(u, args, tab, G);
-      const int blocks = 2 * t.groups / L::kHB;
       // a tile multiplies only the tokens it has (N goes in steps of 16): the rest of its BN rows
       // of X belong to another expert or lie past the end
-      const uint32_t idesc = f16_idesc(kTcBM, (t.cols + 15) / 16 * 16, kBf16);
+      const uint32_t idesc = f16_idesc(kTcBM, (t.cols + 15) / 16 * 16);
       const uint32_t d = tmem + L::kAccCol + buf * BN;
       ok = __all_sync(0xffffffffu, mbar_wait(&dempty[buf], dph ^ 1));   // the epilogue has read it
-      for (int i = 0; i < blocks && ok; ++i) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&afull[as], aph) && mbar_wait(&xfull[s], ph));
+      for (int i = 0; i < t.groups && ok; ++i) {
+        const int as1 = as + 1 == NA ? 0 : as + 1;   // the group's second A stage (kHB = 1)
+        const uint32_t aph1 = as + 1 == NA ? aph ^ 1u : aph;
+        ok = L::kHB == 2 ? mbar_wait_all(&xfull[s], ph, &afull[as], aph)
+                         : mbar_wait_all(&xfull[s], ph, &afull[as], aph, &afull[as1], aph1);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint64_t xd = sw128_kmajor_desc(smem_u32(smem) + s * L::kXBytes);
-        const uint32_t a = tmem + L::kACol + as * L::kACols;
+        const uint32_t a0 = tmem + L::kACol + as * L::kACols;
+        const uint32_t a1 = L::kHB == 2 ? a0 + 32 : tmem + L::kACol + as1 * L::kACols;
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4 * L::kHB; ++k)   // 16 k each: 8 columns of A, 32 bytes of X
-            tc_mma_f16_ta(d, a + 8 * k, xd + (k >> 2) * (L::kXHalf >> 4) + 2 * (k & 3), idesc,
-                          (i | k) != 0 ? 1u : 0u);
+          for (int k = 0; k < 4; ++k)   // 16 k each: 8 columns of A, 32 bytes of X
+            tc_mma_f16_ta(d, a0 + 8 * k, xd + 2 * k, idesc, (i | k) != 0 ? 1u : 0u);
+          if (L::kHB == 1) tc_commit(&aempty[as]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma_f16_ta(d, a1 + 8 * k, xd + (L::kXHalf >> 4) + 2 * k, idesc, 1u);
+          tc_commit(&aempty[L::kHB == 2 ? as : as1]);
           tc_commit(&xempty[s]);
-          tc_commit(&aempty[as]);
-          if (i == blocks - 1) tc_commit(&dfull[buf]);
+          if (i == t.groups - 1) tc_commit(&dfull[buf]);
         }
         __syncwarp();
         if (++s == NX) { s = 0; ph ^= 1; }
-        if (++as == NA) { as = 0; aph ^= 1; }
+        as += 2 / L::kHB;
+        if (as >= NA) { as -= NA; aph ^= 1; }
       }
       if (++buf == 2) { buf = 0; dph ^= 1; }
     }
@@ -375,8 +407,7 @@ __global__ void __launch_bounds__(kTfThreads, 1)
           // groups past K are zero codes that nothing uses; a box is always counted whole
           const int32_t arow = static_cast<int32_t>(t.e * args.N) + t.row0;
           const uint32_t inv_bytes =
-              args.inv_s == nullptr
-                  ? 0u : static_cast<uint32_t>((G - g < kPG ? G - g : kPG) * kGroup * 4);
+              kInv ? static_cast<uint32_t>((G - g < kPG ? G - g : kPG) * kGroup * 4) : 0u;
           mbar_arrive_expect_tx(&pfull[ps], L::kBoxes * L::kBoxBytes + inv_bytes);
 #pragma unroll
           for (int b = 0; b < L::kBoxes; ++b)
@@ -424,14 +455,16 @@ __global__ void __launch_bounds__(kTfThreads, 1)
     int slot_i = 0;         // the ring's current slot is the unit's slot_i-th
     int ps = 0, as = set % NA;
     uint32_t ph = 0, aph = (set / NA) & 1;
+    bool seen = false;      // the current slot's filling has been awaited
     // moves on to slot `to` of the unit: this warp is done with every slot before it (a slot none
     // of whose groups the set has is awaited too, so that each arrival belongs to its filling)
     auto release_to = [&](int to) {
       bool ok = true;
       for (; slot_i < to && ok; ++slot_i) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&pfull[ps], ph));
+        if (!seen) ok = __all_sync(0xffffffffu, mbar_wait(&pfull[ps], ph));
         if (ok && lane == 0) mbar_arrive(&pempty[ps]);
         if (++ps == P) { ps = 0; ph ^= 1; }
+        seen = false;
       }
       return ok;
     };
@@ -466,23 +499,15 @@ __global__ void __launch_bounds__(kTfThreads, 1)
       {
         const int gi = i / kPerG % kPG, h = i % kPerG;   // group of the slot, half of the group
         ok = release_to(i / kPerG / kPG) &&
-             __all_sync(0xffffffffu, mbar_wait(&pfull[ps], ph) && mbar_wait(&aempty[as], aph ^ 1));
+             __all_sync(0xffffffffu, mbar_wait_all(&pfull[ps], ph, &aempty[as], aph ^ 1));
         if (!ok) break;
+        seen = true;
         tc_fence_after();
         const uint8_t* box = smem + L::kPOff + ps * L::kPBytes;
-        const float* inv = args.inv_s == nullptr
-                               ? nullptr
-                               : reinterpret_cast<const float*>(smem + L::kIOff + ps * L::kInvBytes) +
-                                     gi * kGroup + h * kTcBK;
+        const float* inv = reinterpret_cast<const float*>(smem + L::kIOff + ps * L::kInvBytes) +
+                           gi * kGroup + h * kTcBK;   // read with kInv
         const float scf = __half2float(__ushort_as_half(s_cur));
-        uint32_t sc_hi, sc_lo = 0;
-        if constexpr (kBf16) {
-          const float hi = __bfloat162float(__float2bfloat16_rn(scf));
-          sc_hi = float2_to_act2<true>(hi, hi);
-          sc_lo = float2_to_act2<true>(scf - hi, scf - hi);
-        } else {
-          sc_hi = static_cast<uint32_t>(s_cur) * 0x00010001u;
-        }
+        const uint32_t sc = static_cast<uint32_t>(s_cur) * 0x00010001u;
 #pragma unroll
         for (int hh = 0; hh < L::kHB; ++hh) {   // 64 k: 32 columns
           uint32_t wd[2 * kBits];
@@ -510,8 +535,7 @@ __global__ void __launch_bounds__(kTfThreads, 1)
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             uint32_t o[16];
-            dequant32<kBf16, kBits>(wd + q * kBits, z_cur, sc_hi, sc_lo, scf,
-                                    inv == nullptr ? nullptr : inv + 64 * hh + 32 * q, o);
+            dequant32<kBits, kInv>(wd + q * kBits, z_cur, sc, scf, inv + 64 * hh + 32 * q, o);
             tmem_st_32x32b_x16(ta + as * L::kACols + hh * 32 + q * 16, o);
           }
         }
@@ -558,6 +582,12 @@ __global__ void __launch_bounds__(kTfThreads, 1)
         tmem_ld_32x32b_x16(td + buf * BN + c0, v);
         tmem_ld_wait();
         const int nc = cols - c0 < 16 ? cols - c0 : 16;
+        if (args.factors != nullptr) {   // the tokens' factors (prepared activations)
+          const float* f = args.factors + t.m0 + c0;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (j < nc) v[j] = __float_as_uint(__uint_as_float(v[j]) * f[j]);
+        }
         const int64_t y = static_cast<int64_t>(t.m0 + c0) * args.N + n;
         if (live) {
           A* Y = static_cast<A*>(args.Y);

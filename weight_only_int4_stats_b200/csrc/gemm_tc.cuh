@@ -154,7 +154,9 @@ struct TcArgs {
   // grouped launches: M rows of X sorted by expert, N weight rows of each of the E experts
   const int* offsets;   // [E + 1], or NULL for one expert with every row
   int E;
-  FusedEpi epi;         // of the fused products (gemm_fused.cuh)
+  // the fused products (gemm_fused.cuh)
+  FusedEpi epi;
+  const float* factors; // [M]: factors of prepared activations, or NULL
 };
 
 

@@ -27,6 +27,7 @@
 #include "common.cuh"
 #include "fused.cuh"
 #include "gemv.cuh"
+#include "prepare.cuh"
 
 namespace awq {
 
@@ -463,106 +464,6 @@ __global__ void __launch_bounds__(kG4Threads, 2) stream_fused_kernel(
       cur = nxt;
     }
   }
-}
-
-// Rows of X for the kernel above: x' = x inv_s[k] 2^p as fp16 in fragment order, one rounding,
-// p such that the row's largest |x inv_s| lies in [2^14, 2^15) (a value 2^-29 of that and more
-// keeps all of its bits; a row with an infinity or a NaN is taken as it is, p = 0); each
-// group's sum of x' times 2^-24; and the row's factor 2^(24 - p). One CTA per row.
-constexpr int kPrepThreads = 256;
-
-template <bool kBf16>
-__device__ __forceinline__ void prep_load(float (&f)[8], const uint4* X, const float* inv_s, int64_t i) {
-  const uint4 v = X[i];
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 p = act2_to_float2<kBf16>(w[e]);
-    f[2 * e] = p.x;
-    f[2 * e + 1] = p.y;
-  }
-  if (inv_s != nullptr) {
-    const float4 s0 = reinterpret_cast<const float4*>(inv_s)[2 * i];
-    const float4 s1 = reinterpret_cast<const float4*>(inv_s)[2 * i + 1];
-    const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] *= s[e];
-  }
-}
-
-template <bool kBf16>
-__global__ void __launch_bounds__(kPrepThreads) prepare_rows_kernel(
-    const uint4* __restrict__ X, int T, int64_t K, const float* __restrict__ inv_s,
-    const int* __restrict__ offsets, int E, int chunk_groups, int chunk_bytes,
-    uint8_t* __restrict__ out) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int row = blockIdx.x;
-  const int tid = threadIdx.x;
-  if (inv_s != nullptr && offsets != nullptr) {
-    // the row's expert: how many of them end at or before it (every thread counts a few)
-    int e = 0;
-    for (int base = 0; base < E; base += kPrepThreads) {
-      const int i = base + tid;
-      e += __syncthreads_count(i < E && offsets[i + 1] <= row);
-    }
-    if (e >= E) return;   // a row of no expert
-    inv_s += static_cast<int64_t>(e) * K;
-  }
-  const int nch = static_cast<int>(K / 8);
-  const int chunks = (nch / 16 + chunk_groups - 1) / chunk_groups;
-  X += static_cast<int64_t>(row) * nch;
-  float big = 0.0f;
-  bool finite = true;
-  for (int i = tid; i < nch; i += kPrepThreads) {
-    float f[8];
-    prep_load<kBf16>(f, X, inv_s, i);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      big = fmaxf(big, fabsf(f[e]));
-      finite = finite && fabsf(f[e]) <= 3.4028235e38f;
-    }
-  }
-  __shared__ float part[kPrepThreads / 32];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-  if ((tid & 31) == 0) part[tid >> 5] = big;
-  finite = __syncthreads_and(finite);
-#pragma unroll
-  for (int w = 0; w < kPrepThreads / 32; ++w) big = fmaxf(big, part[w]);
-  // 2^14 <= big 2^p < 2^15, from big's exponent; |p| <= 100 keeps both factors normal numbers
-  int p = finite && big > 0.0f ? 14 - (static_cast<int>(__float_as_uint(big) >> 23) - 127) : 0;
-  p = p > 100 ? 100 : p < -100 ? -100 : p;
-  const float up = __uint_as_float(static_cast<uint32_t>(127 + p) << 23);
-  uint8_t* base = out + static_cast<int64_t>(row) * chunks * chunk_bytes;
-  // whole groups (16 lanes each) per iteration: lanes past the row's end take part in the sums
-  for (int i = tid; i < (nch + 31) / 32 * 32; i += kPrepThreads) {
-    float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    const bool live = i < nch;
-    if (live) prep_load<kBf16>(f, X, inv_s, i);
-    uint32_t v[4];
-    float sum = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = float2_to_act2<false>(f[2 * e] * up, f[2 * e + 1] * up);
-      const float2 g = act2_to_float2<false>(v[e]);
-      sum += g.x + g.y;
-    }
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const int g = i >> 4, ch = i & 15;   // 8-k chunk ch of the group: quarter ch / 4, j = ch % 4
-    const int gl = g % chunk_groups;
-    uint8_t* c = base + static_cast<int64_t>(g / chunk_groups) * chunk_bytes;
-    if (live && AWQ_IN_BOUNDS(row < T)) {
-      *reinterpret_cast<uint4*>(c + gl * 256 + (ch & 3) * 64 + (ch >> 2) * 16) =
-          make_uint4(v[0], v[2], v[1], v[3]);   // the pairs of the two MMAs
-      if (ch == 0)
-        *reinterpret_cast<float*>(c + chunk_groups * 256 + gl * 4) = sum * 5.9604644775390625e-8f;
-    }
-  }
-  if (tid == 0)
-    reinterpret_cast<float*>(out + static_cast<int64_t>(T) * chunks * chunk_bytes)[row] =
-        __uint_as_float(static_cast<uint32_t>(127 - p) << 23) * 16777216.0f;
 }
 
 }  // namespace awq
