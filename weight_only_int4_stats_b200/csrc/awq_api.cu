@@ -10,6 +10,7 @@
 #include "awq.h"
 #include "act_stats.cuh"
 #include "common.cuh"
+#include "gated_grouped.cuh"
 #include "gemm_tc.cuh"
 #include "gemv.cuh"
 #include "gemm_fused.cuh"
@@ -85,14 +86,14 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, in
   return r == CUDA_SUCCESS;
 }
 
-template <int BN, ASrc kA, Epi kEpi, bool kBf16, int kBlkT, bool kGrp = false>
+template <int BN, ASrc kA, Epi kEpi, bool kBf16, int kBlkT>
 awq_status launch_tc_blk(const void* Xop, int64_t M, const void* Aop, int64_t a_rows,
                          const awq::TcArgs& args, cudaStream_t st, const void* Aop2) {
-  using L = awq::TcLayout<BN, kA, kBlkT, kGrp>;
+  using L = awq::TcLayout<BN, kA, kBlkT>;
   static std::atomic<bool> attr_set[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return AWQ_ERR_CUDA;
-  auto kern = awq::tc_gemm_kernel<BN, kA, kEpi, kBf16, kBlkT, kGrp>;
+  auto kern = awq::tc_gemm_kernel<BN, kA, kEpi, kBf16, kBlkT>;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem) !=
         cudaSuccess)
@@ -143,10 +144,6 @@ awq_status launch_tc_blk(const void* Xop, int64_t M, const void* Aop, int64_t a_
   }
   a.m_tiles = static_cast<int>((M + BN - 1) / BN);
   a.row_tiles = static_cast<int>((a_rows + awq::kTcBM - 1) / awq::kTcBM);
-  if (kGrp) {   // the row tiles of one expert, and the most token tiles that E experts can have
-    a.row_tiles = static_cast<int>((args.N + awq::kTcBM - 1) / awq::kTcBM);
-    a.m_tiles = static_cast<int>(M / BN + (M < args.E ? M : args.E));
-  }
   a.rows_total = a_rows;
   if (a.k_splits < 1) a.k_splits = 1;
   const int64_t units = static_cast<int64_t>(a.m_tiles) * a.row_tiles * a.k_splits;
@@ -173,17 +170,16 @@ awq_status launch_tc_blk(const void* Xop, int64_t M, const void* Aop, int64_t a_
 // thread set the pace: token tiles up to 128, and inv_s folded into the weights. Plain
 // BN = 256 keeps four one-block stages (two two-block stages, all that fit, measured slower
 // there: 1294 -> 1172 TFLOP/s on [28672, 8192] at M = 4096).
-template <int BN, ASrc kA, Epi kEpi, bool kBf16 = false, bool kGrp = false>
+template <int BN, ASrc kA, Epi kEpi, bool kBf16 = false>
 awq_status launch_tc(const void* Xop, int64_t M, const void* Aop, int64_t a_rows,
                      const awq::TcArgs& args, cudaStream_t st, const void* Aop2 = nullptr) {
   constexpr bool kPk = kA == ASrc::kPacked4 || kA == ASrc::kPacked3;
   if constexpr (kPk && BN == 256) {
     if (args.inv_s == nullptr)
-      return launch_tc_blk<BN, kA, kEpi, kBf16, 1, kGrp>(Xop, M, Aop, a_rows, args, st, Aop2);
-    return launch_tc_blk<BN, kA, kEpi, kBf16, 2, kGrp>(Xop, M, Aop, a_rows, args, st, Aop2);
+      return launch_tc_blk<BN, kA, kEpi, kBf16, 1>(Xop, M, Aop, a_rows, args, st, Aop2);
+    return launch_tc_blk<BN, kA, kEpi, kBf16, 2>(Xop, M, Aop, a_rows, args, st, Aop2);
   } else {
-    return launch_tc_blk<BN, kA, kEpi, kBf16, kPk ? 2 : 1, kGrp>(Xop, M, Aop, a_rows, args, st,
-                                                                 Aop2);
+    return launch_tc_blk<BN, kA, kEpi, kBf16, kPk ? 2 : 1>(Xop, M, Aop, a_rows, args, st, Aop2);
   }
 }
 
@@ -194,19 +190,6 @@ awq_status launch_tc_bn(const void* Xop, int64_t M, const void* Aop, int64_t a_r
   if (M <= 64) return launch_tc<64, kA, kEpi, kBf16>(Xop, M, Aop, a_rows, args, st, Aop2);
   if (M <= 128) return launch_tc<128, kA, kEpi, kBf16>(Xop, M, Aop, a_rows, args, st, Aop2);
   return launch_tc<256, kA, kEpi, kBf16>(Xop, M, Aop, a_rows, args, st, Aop2);
-}
-
-// The gated product of grouped rows: the token tile by the mean rows of an expert. (A tile
-// multiplies only the tokens its expert has, so an expert with fewer wastes no MMA work.)
-awq_status launch_silu_grouped(const void* X, int64_t T, const void* gate, const void* up,
-                               int64_t rows, const awq::TcArgs& args, cudaStream_t st) {
-  constexpr ASrc kA = ASrc::kPair16;
-  constexpr Epi kE = Epi::kSiluMul;
-  const int64_t mean = (T + args.E - 1) / args.E;
-  if (mean <= 32) return launch_tc<32, kA, kE, false, true>(X, T, gate, rows, args, st, up);
-  if (mean <= 64) return launch_tc<64, kA, kE, false, true>(X, T, gate, rows, args, st, up);
-  if (mean <= 128) return launch_tc<128, kA, kE, false, true>(X, T, gate, rows, args, st, up);
-  return launch_tc<256, kA, kE, false, true>(X, T, gate, rows, args, st, up);
 }
 
 // Streaming decode GEMM (M <= 16), launched with programmatic dependent launch.
@@ -339,8 +322,8 @@ int tc_bn_for(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 :
 // pipeline fill, an epilogue and 8 bytes of fp32 partial sums per output to reduce. On the
 // batched shapes 12% measured best among 2, 6, 12, 40 and 60% (e.g. [14336, 4096] at M = 32
 // runs unsplit, 26.6 -> 24.3 us; [4096, 14336] takes 4 slices instead of 9).
-int splitk_for(int64_t M, int64_t N, int64_t K) {
-  const int64_t bn = tc_bn_for(M);
+int splitk_for(int64_t M, int64_t N, int64_t K, int64_t bn = 0) {
+  if (bn == 0) bn = tc_bn_for(M);
   const int64_t tiles = ((N + awq::kTcBM - 1) / awq::kTcBM) * ((M + bn - 1) / bn);
   const int64_t sms = num_sms();
   if (tiles >= sms) return 1;
@@ -867,6 +850,16 @@ awq_status launch_pdl(void (*kern)(KArgs...), dim3 grid, int threads, int smem, 
   return launch_status();
 }
 
+// The tensor-core kernel's token tile. Each token tile dequantizes the weight again, so: one that
+// holds all rows where it can, and equal ones where it cannot; with experts half as much again as
+// the mean row count, which differs from expert to expert (8 experts of [14336, 4096] with 512
+// rows, 52 to 75 each: 143 us with tiles of 64, 113 with 128).
+int tensor_bn(int64_t T, int64_t E) {
+  const int64_t tiles = (T + 191) / 192;
+  const int64_t rows = E == 1 ? (T + tiles - 1) / tiles : (T + E - 1) / E * 3 / 2;
+  return rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 192;
+}
+
 // Which product kernel a call takes, from its shape alone, and the streaming kernel's variant.
 struct FusedPlan {
   enum Kind { kDecode, kStream, kTensor } kind;
@@ -967,14 +960,14 @@ FusedPlan fused_plan(int64_t T, int64_t E, int64_t N, int64_t K, bool grouped) {
   p.kind = FusedPlan::kTensor;
   // prepared activations (bf16) and their factors, then the partial sums of K slices
   p.prepared = align256(static_cast<size_t>(T) * (2 * K + sizeof(float)));
-  p.splits = grouped ? 1 : splitk_for(T, N, K);
+  p.splits = grouped ? 1 : splitk_for(T, N, K, tensor_bn(T, 1));
   p.workspace = p.prepared +
                 (p.splits > 1 ? align256(static_cast<size_t>(p.splits) * T * N * sizeof(float)) : 0);
   return p;
 }
 
 template <int BN, bool kBf16, int kBits, bool kInv>
-awq_status launch_tensor_bn(const void* X, const uint32_t* qweight, awq::TcArgs a, int early,
+awq_status launch_tensor_bn(const void* X, const uint32_t* qweight, awq::FusedArgs a, int early,
                             cudaStream_t st) {   // X fp16, whatever Y's type
   using L = awq::TfLayout<BN, kBits>;
   static std::atomic<bool> attr_set[kMaxDevices] = {};
@@ -1002,13 +995,8 @@ awq_status launch_tensor_bn(const void* X, const uint32_t* qweight, awq::TcArgs 
                     L::kSmem, st, tx, tw, a, early);
 }
 
-int tensor_bn(int64_t T, int64_t E) {
-  const int64_t mean = (T + E - 1) / E;
-  return mean <= 32 ? 32 : mean <= 64 ? 64 : mean <= 128 ? 128 : 192;
-}
-
 template <bool kBf16, int kBits, bool kInv = false>
-awq_status launch_tensor(const void* X, const uint32_t* qweight, const awq::TcArgs& a, int early,
+awq_status launch_tensor(const void* X, const uint32_t* qweight, const awq::FusedArgs& a, int early,
                          cudaStream_t st) {
   switch (tensor_bn(a.M, a.E)) {
     case 32: return launch_tensor_bn<32, kBf16, kBits, kInv>(X, qweight, a, early, st);
@@ -1065,10 +1053,9 @@ awq_status fused_gemm(const void* X, int64_t T, const int32_t* offsets, int64_t 
     return bits == 3 ? launch_stream_plan<false, 3>(plan, X, inv_s, qweight, a, workspace, st)
                      : launch_stream_plan<false, 4>(plan, X, inv_s, qweight, a, workspace, st);
   }
-  awq::TcArgs args{};
+  awq::FusedArgs args{};
   args.M = T;
   args.N = N;
-  args.N_pad = N;
   args.K = K;
   args.scales = reinterpret_cast<const __half*>(scales);
   args.zeros = zeros;
@@ -1102,10 +1089,38 @@ awq_status fused_gemm(const void* X, int64_t T, const int32_t* offsets, int64_t 
     r = bits == 3 ? launch_tensor<false, 3>(X, qweight, args, early, st)
                   : launch_tensor<false, 4>(X, qweight, args, early, st);
   if (r != AWQ_OK || plan.splits == 1) return r;
-  const unsigned grid = static_cast<unsigned>((T * N + 255) / 256);
-  if (bf16) awq::splitk_fused_kernel<true><<<grid, 256, 0, st>>>(args);
-  else awq::splitk_fused_kernel<false><<<grid, 256, 0, st>>>(args);
-  return launch_status();
+  const dim3 grid(static_cast<unsigned>((N + 255) / 256), static_cast<unsigned>(T));
+  return bf16 ? launch_pdl(awq::splitk_fused_kernel<true>, grid, 256, 0, st, args)
+              : launch_pdl(awq::splitk_fused_kernel<false>, grid, 256, 0, st, args);
+}
+
+template <int BN>
+awq_status launch_gated(const void* X, const void* gate, const void* up, awq::FusedArgs a,
+                        cudaStream_t st) {
+  using L = awq::GgLayout<BN>;
+  static std::atomic<bool> attr_set[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return AWQ_ERR_CUDA;
+  auto kern = awq::gated_grouped_kernel<BN>;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem) !=
+        cudaSuccess)
+      return AWQ_ERR_CUDA;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  CUtensorMap tx, tg, tu;
+  if (!make_tmap_2d(&tx, X, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.M, a.K, BN, awq::kTcBK, true) ||
+      !make_tmap_2d(&tg, gate, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.E * a.N, a.K, awq::kTcBM,
+                    awq::kTcBK, true) ||
+      !make_tmap_2d(&tu, up, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.E * a.N, a.K, awq::kTcBM,
+                    awq::kTcBK, true))
+    return AWQ_ERR_CUDA;
+  a.row_tiles = static_cast<int>((a.N + awq::kTcBM - 1) / awq::kTcBM);
+  const int64_t units = a.row_tiles * (a.M / BN + (a.M < a.E ? a.M : a.E));
+  if (units > kMaxDim) return AWQ_ERR_INVALID_ARG;   // the kernel counts them in 32 bits
+  const int64_t sms = num_sms();
+  return launch_pdl(kern, dim3(static_cast<unsigned>(units < sms ? units : sms)), awq::kGgThreads,
+                    L::kSmem, st, tx, tg, tu, a);
 }
 
 bool bad_groups(int64_t E, const int32_t* offsets) {
@@ -1163,16 +1178,20 @@ awq_status awq_silu_mul_gemm_grouped(const awq_f16* X, int64_t T, const int32_t*
   if (!aligned16(X) || !aligned16(W_gate) || !aligned16(W_up) || !aligned16(H))
     return AWQ_ERR_INVALID_ARG;
   if (E * I > kMaxDim) return AWQ_ERR_INVALID_ARG;
-  awq::TcArgs args{};
+  awq::FusedArgs args{};
   args.M = T;
   args.N = I;
-  args.N_pad = I;
   args.K = K;
   args.Y = H;
   args.k_splits = 1;
   args.offsets = offsets;
   args.E = static_cast<int>(E);
-  return launch_silu_grouped(X, T, W_gate, W_up, E * I, args, static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // the token tile: the smallest that holds an expert of half as many rows again as the mean
+  const int64_t rows = (T + E - 1) / E * 3 / 2;
+  if (rows <= 64) return launch_gated<64>(X, W_gate, W_up, args, st);
+  if (rows <= 128) return launch_gated<128>(X, W_gate, W_up, args, st);
+  return launch_gated<256>(X, W_gate, W_up, args, st);
 }
 
 // ------------------------------------------------------------------ act_stats of each expert
@@ -1200,14 +1219,14 @@ awq_status awq_act_stats_grouped(const awq_f16* X, int64_t T, const int32_t* off
     const int64_t slices = awq::grouped_stats_slices(T, K, num_sms());
     dim3 g1(static_cast<unsigned>((K + awq::kStatsCols - 1) / awq::kStatsCols),
             static_cast<unsigned>(slices));
-    awq::act_stats_grouped_partial_kernel<<<g1, 256, 0, st>>>(
-        reinterpret_cast<const __half*>(X), T, K, offsets, static_cast<int>(E), rows, part);
-    awq_status s = launch_status();
+    const awq_status s = launch_pdl(awq::act_stats_grouped_partial_kernel, g1, 256, 0, st,
+                                    reinterpret_cast<const __half*>(X), T, K, offsets,
+                                    static_cast<int>(E), rows, part);
     if (s != AWQ_OK) return s;
   }
   dim3 g2(static_cast<unsigned>((K + 255) / 256), static_cast<unsigned>(E));
-  awq::act_stats_grouped_finish_kernel<<<g2, 256, 0, st>>>(part, T, K, offsets, rows, s_x);
-  return launch_status();
+  return launch_pdl(awq::act_stats_grouped_finish_kernel, g2, 256, 0, st,
+                    static_cast<const double*>(part), T, K, offsets, rows, s_x);
 }
 
 }  // extern "C"

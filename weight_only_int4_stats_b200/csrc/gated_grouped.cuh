@@ -1,0 +1,183 @@
+// K8: the gated product of rows grouped by expert, H = silu(X W_gate[e]^T) * (X W_up[e]^T), with
+// full-precision (fp16) weights: the calibration input of the experts' down projections.
+//
+// Tensor-bound. One tile is 128 rows of both weights (two A tiles and two TMEM accumulators)
+// against up to BN tokens of one expert; units (expert, row tile, token tile) go round the
+// persistent CTAs in gemm_fused.cuh's order, and the whole MMA warp walks the issue loop.
+//   warp 0       TMA producer of X and both weights, in stages of 64 k
+//   warp 1       TMEM allocator and MMA issuer
+//   warps 2, 3   idle
+//   warps 4..11  epilogue: two warps per TMEM lane quarter, each half of the token columns (with
+//                BN = 256 the accumulators fill TMEM, so the next tile waits for this one's
+//                epilogue: eight warps and the fast exponential and division keep that short)
+#pragma once
+#include "common.cuh"
+#include "fused.cuh"
+#include "gemm_fused.cuh"
+
+namespace awq {
+
+constexpr int kGgThreads = 12 * 32;
+constexpr int kGgEpiWarp0 = 4;
+
+template <int BN>
+struct GgLayout {
+  static constexpr int kXBytes = BN * kTcBK * 2;
+  static constexpr int kABytes = kTcBM * kTcBK * 2;          // of one weight
+  static constexpr int kStage = kXBytes + 2 * kABytes;
+  static constexpr int kStages = BN == 256 ? 3 : BN == 128 ? 4 : 5;
+  static constexpr int kBufs = 4 * BN <= 512 ? 2 : 1;        // accumulator pairs in TMEM
+  static constexpr uint32_t kCols = 2 * BN * kBufs;
+  static constexpr int kBarOff = kStages * kStage;
+  static constexpr int kTabOff = kBarOff + 256;
+  static constexpr int kSmem = kTabOff + static_cast<int>(sizeof(GroupTable)) + 1024;
+  static_assert(kSmem <= kTcSmemMax && (2 * kStages + 4) * 8 + 8 <= 256, "shared memory");
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kGgThreads, 1)
+    gated_grouped_kernel(const __grid_constant__ CUtensorMap tmap_x,
+                         const __grid_constant__ CUtensorMap tmap_g,
+                         const __grid_constant__ CUtensorMap tmap_u, const FusedArgs args) {
+  using L = GgLayout<BN>;
+  constexpr int S = L::kStages, B = L::kBufs;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* empty = full + S;
+  uint64_t* dfull = empty + S;
+  uint64_t* dempty = dfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dempty + 2);
+  GroupTable* tab = reinterpret_cast<GroupTable*>(smem + L::kTabOff);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int G = static_cast<int>(args.K / kGroup);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&dfull[i], 1);
+      mbar_init(&dempty[i], 8);   // every epilogue warp
+    }
+    fence_barrier_init();
+    tma_prefetch_desc(&tmap_x);
+    tma_prefetch_desc(&tmap_g);
+    tma_prefetch_desc(&tmap_u);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, L::kCols);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (warp == 0) build_group_table(tab->off, tab->tile, args.offsets, args.E, args.M, BN);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const unsigned units =
+      static_cast<unsigned>(args.row_tiles) * static_cast<unsigned>(tab->tile[args.E]);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ producer
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (unsigned u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        const TfUnit t = tf_unit<BN>(u, args, tab, G);
+        const int arow = static_cast<int>(t.e * args.N) + t.row0;
+        for (int i = 0; i < 2 * G; ++i) {
+          ok = mbar_wait(&empty[s], ph ^ 1);
+          if (!ok) break;
+          uint8_t* st = smem + s * L::kStage;
+          mbar_arrive_expect_tx(&full[s], L::kStage);
+          tma_load_2d(st, &tmap_x, &full[s], i * kTcBK, t.m0);
+          tma_load_2d(st + L::kXBytes, &tmap_g, &full[s], i * kTcBK, arow);
+          tma_load_2d(st + L::kXBytes + L::kABytes, &tmap_u, &full[s], i * kTcBK, arow);
+          if (++s == S) { s = 0; ph ^= 1; }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    int s = 0, buf = 0;
+    uint32_t ph = 0, dph = 0;
+    bool ok = true;
+    for (unsigned u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const TfUnit t = tf_unit<BN>(u, args, tab, G);
+      const uint32_t idesc = f16_idesc(kTcBM, (t.cols + 15) / 16 * 16);
+      const uint32_t d = tmem + buf * 2 * BN;
+      ok = __all_sync(0xffffffffu, mbar_wait(&dempty[buf], dph ^ 1));
+      for (int i = 0; i < 2 * G && ok; ++i) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[s], ph));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t st = smem_u32(smem) + s * L::kStage;
+        const uint64_t xd = sw128_kmajor_desc(st);
+        const uint64_t gd = sw128_kmajor_desc(st + L::kXBytes);
+        const uint64_t ud = sw128_kmajor_desc(st + L::kXBytes + L::kABytes);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            tc_mma_f16(d, gd + 2 * k, xd + 2 * k, idesc, (i | k) != 0 ? 1u : 0u);
+            tc_mma_f16(d + BN, ud + 2 * k, xd + 2 * k, idesc, (i | k) != 0 ? 1u : 0u);
+          }
+          tc_commit(&empty[s]);
+          if (i == 2 * G - 1) tc_commit(&dfull[buf]);
+        }
+        __syncwarp();
+        if (++s == S) { s = 0; ph ^= 1; }
+      }
+      if (++buf == B) { buf = 0; dph ^= 1; }
+    }
+  } else if (warp >= kGgEpiWarp0) {
+    // ------------------------------------------------------------------ epilogue
+    const int half = (warp - kGgEpiWarp0) >> 2;
+    const int row = 32 * (warp & 3) + lane;
+    const uint32_t td = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    __half* H = static_cast<__half*>(args.Y);
+    int buf = 0;
+    uint32_t ph = 0;
+    for (unsigned u = blockIdx.x; u < units; u += gridDim.x) {
+      const TfUnit t = tf_unit<BN>(u, args, tab, G);
+      const int64_t n = t.row0 + row;
+      const bool live = n < args.N && AWQ_IN_BOUNDS(t.m0 + t.cols <= args.M && t.e < args.E);
+      if (!__all_sync(0xffffffffu, mbar_wait(&dfull[buf], ph))) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c0 = 16 * half; c0 < t.cols; c0 += 32) {
+        uint32_t g[16], v[16];
+        tmem_ld_32x32b_x16(td + buf * 2 * BN + c0, g);
+        tmem_ld_32x32b_x16(td + buf * 2 * BN + BN + c0, v);
+        tmem_ld_wait();
+        if (live) {
+          __half* h = H + static_cast<int64_t>(t.m0 + c0) * args.N + n;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c0 + j < t.cols)
+              h[j * args.N] = __float2half_rn(activate(__uint_as_float(g[j]), kActSilu) *
+                                              __uint_as_float(v[j]));
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&dempty[buf]);
+      if (++buf == B) { buf = 0; ph ^= 1; }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kCols);
+  }
+}
+
+}  // namespace awq

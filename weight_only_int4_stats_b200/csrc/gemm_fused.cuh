@@ -37,6 +37,7 @@
 #include "common.cuh"
 #include "fused.cuh"
 #include "gemm_tc.cuh"
+#include "gemv.cuh"
 #include "prepare.cuh"
 
 namespace awq {
@@ -135,15 +136,30 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+struct FusedArgs {
+  int64_t M, N, K;          // rows of X and Y; weight rows of an expert
+  int E;
+  int row_tiles;            // 128-row tiles of an expert's weight
+  int k_splits;             // > 1: a unit takes a slice of K's groups
+  const int* offsets;       // [E + 1], or NULL for one expert with every row
+  const __half* scales;     // [E, K / 128, N]
+  const uint8_t* zeros;
+  const float* inv_s;       // [E, K] or NULL
+  const float* factors;     // [M]: factors of prepared activations, or NULL
+  float* partial;           // [k_splits, M, N]
+  FusedEpi epi;
+  void* Y;
+};
+
 // A work unit: K slice, expert, row tile and token tile, and the slice's groups.
 struct TfUnit {
   int e, row0, m0, cols;      // expert, first weight row, first token, its tokens (at most BN)
   int g0, groups, ksplit;
 };
 // Unit u (32-bit: see the launch). Units of a slice sweep the token tiles of 16 row tiles at a
-// time (tile_of_block's order).
+// time (so the units in flight share a few weight and token tiles in L2).
 template <int BN>
-__device__ __forceinline__ TfUnit tf_unit(unsigned u, const TcArgs& a, const GroupTable* tab, int G) {
+__device__ __forceinline__ TfUnit tf_unit(unsigned u, const FusedArgs& a, const GroupTable* tab, int G) {
   TfUnit t;
   const unsigned rt = static_cast<unsigned>(a.row_tiles);
   const unsigned tiles = rt * static_cast<unsigned>(tab->tile[a.E]);
@@ -268,7 +284,7 @@ __device__ __forceinline__ void fused_columns(const FusedEpi& f, act_t<kBf16>* Y
 template <int BN, bool kBf16, int kBits, bool kInv>
 __global__ void __launch_bounds__(kTfThreads, 1)
     tc_fused_kernel(const __grid_constant__ CUtensorMap tmap_x,
-                    const __grid_constant__ CUtensorMap tmap_w, const TcArgs args, const int early) {
+                    const __grid_constant__ CUtensorMap tmap_w, const FusedArgs args, const int early) {
   using L = TfLayout<BN, kBits>;
   constexpr int NX = L::kXStages, NA = L::kNA, P = L::kPSlots, kPG = L::kPG;
   extern __shared__ uint8_t smem_raw[];
@@ -637,6 +653,23 @@ __global__ void __launch_bounds__(kTfThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// The epilogue on the sum over the K slices of the fp32 partial sums, slices added in order. One
+// CTA per 256 outputs of a row of Y; the first loads of the epilogue's operands are in flight
+// with those of the partial sums.
+template <bool kBf16>
+__global__ void __launch_bounds__(256) splitk_fused_kernel(const FusedArgs args) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (n >= args.N) return;
+  const int64_t i = static_cast<int64_t>(blockIdx.y) * args.N + n, MN = args.M * args.N;
+  FusedIn<kBf16> in;
+  in.load(args.epi, n, blockIdx.y, args.N, static_cast<int>(args.M));
+  float acc = args.partial[i];
+  for (int s = 1; s < args.k_splits; ++s) acc += args.partial[s * MN + i];
+  static_cast<act_t<kBf16>*>(args.Y)[i] = float_to_act<kBf16>(in.apply(args.epi, acc, 0));
 }
 
 }  // namespace awq

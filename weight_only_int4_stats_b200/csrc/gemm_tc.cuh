@@ -38,7 +38,6 @@
 // leave their loops so the CTA still releases its TMEM and exits.
 #pragma once
 #include "common.cuh"
-#include "fused.cuh"
 
 namespace awq {
 
@@ -73,7 +72,7 @@ enum class ASrc : int { kPacked4 = 0, kPacked3 = 1, kSplit16 = 2, kPair16 = 3, k
 // D[n][j] * e'[n][j], the recombined product times the row's own error operand.
 enum class Epi : int { kStoreY = 0, kRowSumSq = 1, kSiluMul = 2, kStoreF32 = 3, kGramDot = 4 };
 
-template <int BN, ASrc kA, int kBlkT = 1, bool kGrp = false>
+template <int BN, ASrc kA, int kBlkT = 1>
 struct TcLayout {
   static constexpr bool kPk = kA == ASrc::kPacked4 || kA == ASrc::kPacked3;
   static constexpr int kXParts = kA == ASrc::kGram ? 2 : 1;   // B tiles per stage
@@ -107,8 +106,7 @@ struct TcLayout {
   // as many packed slots as the shared memory left by the stages holds (1024 bytes of
   // alignment slack and 512 of barriers reserved)
   static constexpr int kPFit =
-      (kTcSmemMax - (kGrp ? static_cast<int>(sizeof(GroupTable)) : 0) - 1024 - 512 -
-       kStages * (kXBytes + kABytes)) /
+      (kTcSmemMax - 1024 - 512 - kStages * (kXBytes + kABytes)) /
       (kPBytes + kSZBytes + kInvBytes);
   static constexpr int kPSlots =
       !kPk ? 0 : (kPFit < kTcPkSlotsMax ? kPFit : kTcPkSlotsMax);
@@ -120,8 +118,7 @@ struct TcLayout {
   static constexpr int kIOff = kSZOff + kPSlots * kSZBytes;
   static constexpr int kBarOff = kIOff + kPSlots * kInvBytes;
   // full[S], empty[S], built[S], pfull[P], pempty[P], acc_full[2], acc_empty[2], tmem slot
-  static constexpr int kTabOff = kBarOff + (3 * kStages + 2 * kPBars + 4) * 8 + 16;
-  static constexpr int kBytes = kTabOff + (kGrp ? static_cast<int>(sizeof(GroupTable)) : 0);
+  static constexpr int kBytes = kBarOff + (3 * kStages + 2 * kPBars + 4) * 8 + 16;
   static constexpr int kSmem = kBytes + 1024;   // slack for 1024-byte alignment
   static constexpr uint32_t kTxBytes = kXBytes + (kPk ? 0 : kABytes);
   // one accumulator per A part, double-buffered when TMEM's 512 columns allow (so a tile's
@@ -151,14 +148,7 @@ struct TcArgs {
   int upper_only;       // kStoreF32: compute only the tiles that reach the diagonal or above it
                         // (G is symmetric; readers take G[min(i,j)][max(i,j)])
   const __half* E2;     // kGramDot: the error operand [rows_total, 2K] the epilogue reads
-  // grouped launches: M rows of X sorted by expert, N weight rows of each of the E experts
-  const int* offsets;   // [E + 1], or NULL for one expert with every row
-  int E;
-  // the fused products (gemm_fused.cuh)
-  FusedEpi epi;
-  const float* factors; // [M]: factors of prepared activations, or NULL
 };
-
 
 // Grouped tile order: consecutive work units sweep the token tiles of a group of
 // kTcRasterRows weight-row tiles, so the units in flight at one time share a few A tiles and
@@ -178,35 +168,13 @@ __device__ __forceinline__ void tile_of_block(int64_t bid, int row_tiles, int m_
 
 struct TcUnit {
   int row_tile, m_tile, ksplit, kb0, nkb;
-  int e;             // expert
-  int64_t m0;        // first token, and one past the last token the unit may use
-  int64_t m_end;
 };
 
-// `e` is the caller's cursor: the expert of its last unit (units of a slice come in order).
-template <int BN, bool kGrp>
-__device__ __forceinline__ TcUnit unit_of(int64_t u, const TcArgs& a, const GroupTable* tab,
-                                          int& e) {
+__device__ __forceinline__ TcUnit unit_of(int64_t u, const TcArgs& a) {
   TcUnit t;
-  if constexpr (kGrp) {
-    const int64_t tiles = static_cast<int64_t>(a.row_tiles) * tab->tile[a.E];
-    t.ksplit = static_cast<int>(u / tiles);
-    const int64_t v = u % tiles;
-    if (v < static_cast<int64_t>(a.row_tiles) * tab->tile[e]) e = 0;   // a new slice of K
-    while (v >= static_cast<int64_t>(a.row_tiles) * tab->tile[e + 1]) ++e;
-    tile_of_block(v - static_cast<int64_t>(a.row_tiles) * tab->tile[e], a.row_tiles,
-                  tab->tile[e + 1] - tab->tile[e], t.row_tile, t.m_tile);
-    t.e = e;
-    t.m0 = tab->off[e] + static_cast<int64_t>(t.m_tile) * BN;
-    t.m_end = tab->off[e + 1];
-  } else {
-    const int64_t tiles = static_cast<int64_t>(a.row_tiles) * a.m_tiles;
-    t.ksplit = static_cast<int>(u / tiles);
-    tile_of_block(u % tiles, a.row_tiles, a.m_tiles, t.row_tile, t.m_tile);
-    t.e = 0;
-    t.m0 = static_cast<int64_t>(t.m_tile) * BN;
-    t.m_end = a.M;
-  }
+  const int64_t tiles = static_cast<int64_t>(a.row_tiles) * a.m_tiles;
+  t.ksplit = static_cast<int>(u / tiles);
+  tile_of_block(u % tiles, a.row_tiles, a.m_tiles, t.row_tile, t.m_tile);
   const int G = static_cast<int>(a.K / kGroup);
   const int kb0 = 2 * static_cast<int>(static_cast<int64_t>(t.ksplit) * G / a.k_splits);
   const int kb1 = 2 * static_cast<int>(static_cast<int64_t>(t.ksplit + 1) * G / a.k_splits);
@@ -299,19 +267,18 @@ __device__ __forceinline__ uint32_t sw128_offset(int r, int c) {
   return static_cast<uint32_t>((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
 }
 
-template <int BN, ASrc kA, Epi kEpi, bool kBf16 = false, int kBlkT = 1, bool kGrp = false>
+template <int BN, ASrc kA, Epi kEpi, bool kBf16 = false, int kBlkT = 1>
 __global__ void __launch_bounds__(kTcThreads, 1)
     tc_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x,
                    const __grid_constant__ CUtensorMap tmap_a,
                    const __grid_constant__ CUtensorMap tmap_s,
                    const __grid_constant__ CUtensorMap tmap_z, const TcArgs args) {
-  using L = TcLayout<BN, kA, kBlkT, kGrp>;
+  using L = TcLayout<BN, kA, kBlkT>;
   constexpr int S = L::kStages;
   constexpr bool kPacked = L::kPk;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  GroupTable* tab = reinterpret_cast<GroupTable*>(smem + L::kTabOff);   // grouped launches
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* empty = full + S;
   uint64_t* built = empty + S;
@@ -325,9 +292,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   static_assert(kEpi != Epi::kSiluMul || kA == ASrc::kPair16,
                 "the SiLU epilogue combines the gate and up accumulators");
   static_assert(kEpi != Epi::kStoreY || kPacked, "fp16 Y comes from the packed sources");
-  static_assert(!kGrp || kEpi == Epi::kSiluMul, "the gated products have a grouped form");
   static_assert(L::kSmem <= kTcSmemMax, "shared memory layout too large");
-
   uint64_t* pempty = pfull + P;
   uint64_t* acc_full = pempty + P;
   uint64_t* acc_empty = acc_full + 2;
@@ -335,7 +300,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  int64_t units = static_cast<int64_t>(args.row_tiles) * args.m_tiles * args.k_splits;
+  const int64_t units =
+      static_cast<int64_t>(args.row_tiles) * args.m_tiles * args.k_splits;
   if (kEpi == Epi::kStoreF32 && args.upper_only) {
     // One CTA per output tile: a tile whose rows all lie below its columns (every element
     // G[i][j] with i > j) is the transpose of a computed one, so its CTA has nothing to do.
@@ -382,12 +348,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // behind this one overlaps this kernel alone, never an earlier one).
   pdl_wait();
   pdl_launch_dependents();
-  if constexpr (kGrp) {
-    if (warp == 0) build_group_table(tab->off, tab->tile, args.offsets, args.E, args.M, BN);
-    __syncthreads();
-    units = static_cast<int64_t>(args.row_tiles) * tab->tile[args.E] * args.k_splits;
-  }
-  int expert = 0;   // this thread's cursor over the experts
 
   if (warp == kTcXWarp) {
     // ------------------------------------------------------------------ TMA producer
@@ -396,9 +356,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       uint32_t ph = 0;
       bool ok = true;
       for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        const TcUnit t = unit_of<BN, kGrp>(u, args, tab, expert);
-        const int64_t m0 = t.m0;
-        const int64_t row0 = static_cast<int64_t>(t.row_tile) * kTcBM + (kGrp ? t.e * args.N : 0);
+        const TcUnit t = unit_of(u, args);
+        const int64_t m0 = static_cast<int64_t>(t.m_tile) * BN;
+        const int64_t row0 = static_cast<int64_t>(t.row_tile) * kTcBM;
         for (int i = 0; i < t.nkb; i += L::kBlk) {
           const int kb = t.kb0 + i;
           if (!mbar_wait(&empty[s], ph ^ 1)) {
@@ -434,19 +394,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else if (warp == kTcMmaWarp) {
     // ------------------------------------------------------------------ MMA issuer
     if (lane == 0) {
+      constexpr uint32_t idesc = f16_idesc(kTcBM, BN, kBf16);
       int s = 0;
       uint32_t ph = 0;
       int64_t lt = 0;
       bool ok = true;
       for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x, ++lt) {
-        const TcUnit t = unit_of<BN, kGrp>(u, args, tab, expert);
+        const TcUnit t = unit_of(u, args);
         const int buf = static_cast<int>(lt % L::kAccBufs);
         const uint32_t acc_ph = static_cast<uint32_t>((lt / L::kAccBufs) & 1);
-        // a grouped tile multiplies only its expert's tokens (the MMA's N goes in steps of 16);
-        // the rest of its BN token rows belong to the next expert and are left out
-        const int n16 = kGrp && t.m_end - t.m0 < BN
-                            ? static_cast<int>((t.m_end - t.m0 + 15) / 16 * 16) : BN;
-        const uint32_t idesc = f16_idesc(kTcBM, n16, kBf16);
         if (!mbar_wait(&acc_empty[buf], acc_ph ^ 1)) break;   // epilogue released the buffer
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * L::kAParts * BN);
@@ -497,7 +453,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       uint32_t ph = 0, pph = 0;
       bool ok = true;
       for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        const TcUnit tu = unit_of<BN, kGrp>(u, args, tab, expert);
+        const TcUnit tu = unit_of(u, args);
         const int64_t n = static_cast<int64_t>(tu.row_tile) * kTcBM + r;
         // one 128-k group per iteration: the stage's two 64-k blocks are built, then one proxy
         // fence and one arrival (K slices are whole groups, so nkb is even)
@@ -602,27 +558,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int64_t lt = 0;
     bool ok = true;
     for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x, ++lt) {
-      const TcUnit t = unit_of<BN, kGrp>(u, args, tab, expert);
+      const TcUnit t = unit_of(u, args);
       const int buf = static_cast<int>(lt % L::kAccBufs);
       ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf],
                                              static_cast<uint32_t>((lt / L::kAccBufs) & 1)));
       if (!ok) break;
       tc_fence_after();
-      const int64_t m0 = t.m0;
+      const int64_t m0 = static_cast<int64_t>(t.m_tile) * BN;
       const int64_t arow = static_cast<int64_t>(t.row_tile) * kTcBM + row;
-      const int64_t m_end = t.m_end;
-      // the columns the MMA wrote
-      const int cols = kGrp && m_end - m0 < BN ? static_cast<int>(m_end - m0) : BN;
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * wq) << 16) +
                              static_cast<uint32_t>(buf * L::kAParts * BN);
       const bool unit_ok =
-          AWQ_IN_BOUNDS(t.row_tile < args.row_tiles && (kGrp || t.m_tile < args.m_tiles) &&
-                        m_end <= args.M &&
+          AWQ_IN_BOUNDS(t.row_tile < args.row_tiles && t.m_tile < args.m_tiles &&
                         t.ksplit < args.k_splits &&
                         (buf + 1) * L::kAParts * BN <= static_cast<int>(L::kTmemCols));
       double sumsq = 0.0;
 #pragma unroll 1
-      for (int col = 0; col < cols; col += 16) {
+      for (int col = 0; col < BN; col += 16) {
         uint32_t v[16];
         tmem_ld_32x32b_x16(taddr + col, v);
         tmem_ld_wait();
@@ -695,7 +647,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const int64_t m = m0 + col + j;
               const float g = __uint_as_float(v[j]);
               const float h = __fdiv_rn(g * __uint_as_float(vu[j]), 1.0f + expf(-g));
-              if (m < m_end) static_cast<__half*>(args.Y)[m * args.N + arow] = __float2half_rn(h);
+              if (m < args.M) static_cast<__half*>(args.Y)[m * args.N + arow] = __float2half_rn(h);
             }
           }
         } else {
@@ -725,7 +677,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       uint32_t pph = 0;
       bool ok = true;
       for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        const TcUnit t = unit_of<BN, kGrp>(u, args, tab, expert);
+        const TcUnit t = unit_of(u, args);
         const int32_t row0 = t.row_tile * kTcBM;
         // a last slot that runs past the unit's K slice loads groups it does not use (zero
         // filled past K); the transaction count is always the full box
@@ -765,20 +717,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, L::kTmemCols);
   }
-}
-
-// The fused epilogue on the sum over the K slices of the fp32 partial sums, slices added in
-// order. One thread per output of one packed weight.
-template <bool kBf16>
-__global__ void splitk_fused_kernel(const TcArgs args) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int64_t MN = args.M * args.N;
-  if (i >= MN) return;
-  const int64_t n = i % args.N;
-  float acc = args.partial[i];
-  for (int s = 1; s < args.k_splits; ++s) acc += args.partial[s * MN + i];
-  fused_store<kBf16>(args.epi, static_cast<act_t<kBf16>*>(args.Y), i,
-                     acc + fused_bias<kBf16>(args.epi, n));
 }
 
 // Y[m, n] = fp16 (bf16) of the sum over the K slices of the fp32 partial sums, slices added
