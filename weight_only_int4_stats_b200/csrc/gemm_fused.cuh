@@ -89,24 +89,31 @@ __device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, 
       : "memory");
 }
 
-// mbar_wait on two or three barriers at once: their polls are in flight together.
-__device__ __forceinline__ bool mbar_wait_all(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1) {
-  const bool r0 = mbar_try_wait(smem_u32(b0), p0), r1 = mbar_try_wait(smem_u32(b1), p1);
-  return (r0 || mbar_wait(b0, p0)) && (r1 || mbar_wait(b1, p1));
+// Whether the phase of that parity is complete, at once (mbar_try_wait may suspend the thread for
+// a while when it is not).
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
-__device__ __forceinline__ bool mbar_wait_all(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1,
-                                              uint64_t* b2, uint32_t p2) {
-  const bool r0 = mbar_try_wait(smem_u32(b0), p0), r1 = mbar_try_wait(smem_u32(b1), p1),
-             r2 = mbar_try_wait(smem_u32(b2), p2);
-  return (r0 || mbar_wait(b0, p0)) && (r1 || mbar_wait(b1, p1)) && (r2 || mbar_wait(b2, p2));
+
+// mbar_wait on two barriers at once: their first polls are in flight together.
+__device__ __forceinline__ bool mbar_wait_all(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1) {
+  const bool r0 = mbar_test_wait(b0, p0), r1 = mbar_test_wait(b1, p1);
+  return (r0 || mbar_wait(b0, p0)) && (r1 || mbar_wait(b1, p1));
 }
 
 // mbar_wait for a warp that has time: it looks only now and then, so that its polling takes no
 // issue slots from the warps that set the pace.
 __device__ __forceinline__ bool mbar_wait_lazy(uint64_t* bar, uint32_t parity) {
-  const uint32_t a = smem_u32(bar);
   for (int i = 0; i < 64; ++i) {
-    if (mbar_try_wait(a, parity)) return true;
+    if (mbar_test_wait(bar, parity)) return true;
     __nanosleep(256);
   }
   return mbar_wait(bar, parity);
@@ -258,25 +265,92 @@ __device__ __forceinline__ void dequant32(const uint32_t* w, uint32_t z, uint32_
   }
 }
 
-// 8 token columns of one weight row through the epilogue, the activation known at compile
-// time: loads first, then arithmetic, then stores. y: the row's first output of the columns.
+// 16 token columns of one weight row through the epilogue, the activation known at compile time.
+// y: the row's first output of the columns, nc of them are its expert's tokens. With bf16 outputs
+// lane j holds the factor of token j's prepared activations. The epilogue warps share the issue
+// slots with the builders, so what is absent costs nothing here: written with a multiply and an
+// add of a default for each output it took 35,000 cycles a tile of 192 tokens, as much as the
+// tile's products.
 template <bool kBf16, int kAct>
-__device__ __forceinline__ void fused_columns(const FusedEpi& f, act_t<kBf16>* Y, int64_t y, int64_t N,
-                                              int cols, float bias, const uint32_t* v) {
+__device__ __forceinline__ void fused_columns(const FusedArgs& a, int64_t y, int nc, bool live,
+                                              float bias, float factor, uint32_t (&v)[16]) {
   using A = act_t<kBf16>;
-  A mul[8], res[8];
-  const A* pm = static_cast<const A*>(f.mul);
-  const A* pr = static_cast<const A*>(f.residual);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    mul[j] = pm != nullptr && j < cols ? pm[y + j * N] : A(1.0f);
-    res[j] = pr != nullptr && j < cols ? pr[y + j * N] : A(0.0f);
+  for (int j = 0; j < 16; ++j) {
+    float x = __uint_as_float(v[j]);
+    if constexpr (kBf16) x = fmaf(x, __shfl_sync(0xffffffffu, factor, j), bias);
+    else x += bias;
+    v[j] = __float_as_uint(activate(x, kAct));
   }
+  if (!live) return;
+  if (a.epi.mul != nullptr) {
+    const A* p = static_cast<const A*>(a.epi.mul) + y;
+    A m[16];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float p = activate(__uint_as_float(v[j]) + bias, kAct);
-    if (j < cols)
-      Y[y + j * N] = float_to_act<kBf16>(fmaf(p, act_to_float<kBf16>(mul[j]), act_to_float<kBf16>(res[j])));
+    for (int j = 0; j < 16; ++j) m[j] = j < nc ? p[j * a.N] : A(0.0f);
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      v[j] = __float_as_uint(__uint_as_float(v[j]) * act_to_float<kBf16>(m[j]));
+  }
+  if (a.epi.residual != nullptr) {
+    const A* p = static_cast<const A*>(a.epi.residual) + y;
+    A r[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) r[j] = j < nc ? p[j * a.N] : A(0.0f);
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      v[j] = __float_as_uint(__uint_as_float(v[j]) + act_to_float<kBf16>(r[j]));
+  }
+  A* p = static_cast<A*>(a.Y) + y;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if (j < nc) *p = float_to_act<kBf16>(__uint_as_float(v[j]));
+    p += a.N;
+  }
+}
+
+// A warp's share of a tile's token columns (alternate 16), from its TMEM lanes at td.
+template <bool kBf16, int kAct>
+__device__ __forceinline__ void fused_tile(const FusedArgs& a, const TfUnit& t, int64_t n, bool live,
+                                           float bias, int half, int lane, uint32_t td) {
+#pragma unroll 1
+  for (int c0 = 16 * half; c0 < t.cols; c0 += 32) {
+    float factor = 0.0f;
+    if (kBf16 && c0 + (lane & 15) < t.cols) factor = a.factors[t.m0 + c0 + (lane & 15)];
+    uint32_t v[16];
+    tmem_ld_32x32b_x16(td + c0, v);
+    tmem_ld_wait();
+    fused_columns<kBf16, kAct>(a, static_cast<int64_t>(t.m0 + c0) * a.N + n,
+                               t.cols - c0, live, bias, factor, v);
+    __syncwarp();   // the next TMEM load is the whole warp's
+  }
+}
+
+// The same for a slice of K: partial sums, times the factors.
+template <bool kBf16>
+__device__ __forceinline__ void partial_tile(const FusedArgs& a, const TfUnit& t, int64_t n, bool live,
+                                             int half, int lane, uint32_t td) {
+#pragma unroll 1
+  for (int c0 = 16 * half; c0 < t.cols; c0 += 32) {
+    float factor = 1.0f;
+    if (kBf16 && c0 + (lane & 15) < t.cols) factor = a.factors[t.m0 + c0 + (lane & 15)];
+    uint32_t v[16];
+    tmem_ld_32x32b_x16(td + c0, v);
+    tmem_ld_wait();
+    if constexpr (kBf16) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        v[j] = __float_as_uint(__uint_as_float(v[j]) * __shfl_sync(0xffffffffu, factor, j));
+    }
+    if (live) {
+      float* p = a.partial + (static_cast<int64_t>(t.ksplit) * a.M + t.m0 + c0) * a.N + n;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        if (j < t.cols - c0) *p = __uint_as_float(v[j]);
+        p += a.N;
+      }
+    }
+    __syncwarp();
   }
 }
 
@@ -368,9 +442,19 @@ __global__ void __launch_bounds__(kTfThreads, 1)
     // The whole warp walks the loop, so that what the instructions take (descriptors, TMEM
     // addresses) is the same in every lane and lives in uniform registers; one elected lane
     // issues. (A loop that only lane 0 ran issued one MMA in about 80 cycles, whatever its N.)
+    // The next group's barriers are polled before this group's MMAs are issued, so that the
+    // polls' latency passes behind them.
+    const bool leader = elect_one();
+    const uint64_t xd0 = sw128_kmajor_desc(smem_u32(smem));
     int s = 0, as = 0, buf = 0;
     uint32_t ph = 0, aph = 0, dph = 0;
-    bool ok = true;
+    bool ok = true, ready = false;
+    const auto poll = [&]() {   // of stages s, as (kHB = 1: as is even, and as + 1)
+      const bool r0 = mbar_test_wait(&xfull[s], ph);
+      const bool r1 = mbar_test_wait(&afull[as], aph);
+      const bool r2 = L::kHB == 2 || mbar_test_wait(&afull[as + 1], aph);
+      return r0 && r1 && r2;
+    };
     for (unsigned u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const TfUnit t = tf_unit<BN>(u, args, tab, G);
       // a tile multiplies only the tokens it has (N goes in steps of 16): the rest of its BN rows
@@ -379,32 +463,34 @@ __global__ void __launch_bounds__(kTfThreads, 1)
       const uint32_t d = tmem + L::kAccCol + buf * BN;
       ok = __all_sync(0xffffffffu, mbar_wait(&dempty[buf], dph ^ 1));   // the epilogue has read it
       for (int i = 0; i < t.groups && ok; ++i) {
-        const int as1 = as + 1 == NA ? 0 : as + 1;   // the group's second A stage (kHB = 1)
-        const uint32_t aph1 = as + 1 == NA ? aph ^ 1u : aph;
-        ok = L::kHB == 2 ? mbar_wait_all(&xfull[s], ph, &afull[as], aph)
-                         : mbar_wait_all(&xfull[s], ph, &afull[as], aph, &afull[as1], aph1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        if (!__all_sync(0xffffffffu, ready)) {
+          ok = mbar_wait(&xfull[s], ph) && mbar_wait(&afull[as], aph) &&
+               (L::kHB == 2 || mbar_wait(&afull[as + 1], aph));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
         tc_fence_after();
-        const uint64_t xd = sw128_kmajor_desc(smem_u32(smem) + s * L::kXBytes);
-        const uint32_t a0 = tmem + L::kACol + as * L::kACols;
-        const uint32_t a1 = L::kHB == 2 ? a0 + 32 : tmem + L::kACol + as1 * L::kACols;
-        if (elect_one()) {
+        const uint64_t xd = xd0 + static_cast<uint64_t>(s * (L::kXBytes >> 4));
+        const uint32_t a = tmem + L::kACol + as * L::kACols;
+        uint64_t* xe = &xempty[s];
+        uint64_t* ae = &aempty[as];
+        if (++s == NX) { s = 0; ph ^= 1; }
+        as += 2 / L::kHB;
+        if (as == NA) { as = 0; aph ^= 1; }
+        ready = poll();
+        if (leader) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)   // 16 k each: 8 columns of A, 32 bytes of X
-            tc_mma_f16_ta(d, a0 + 8 * k, xd + 2 * k, idesc, (i | k) != 0 ? 1u : 0u);
-          if (L::kHB == 1) tc_commit(&aempty[as]);
+            tc_mma_f16_ta(d, a + 8 * k, xd + 2 * k, idesc, (i | k) != 0 ? 1u : 0u);
+          if (L::kHB == 1) tc_commit(ae);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc_mma_f16_ta(d, a1 + 8 * k, xd + (L::kXHalf >> 4) + 2 * k, idesc, 1u);
-          tc_commit(&aempty[L::kHB == 2 ? as : as1]);
-          tc_commit(&xempty[s]);
+            tc_mma_f16_ta(d, a + 32 + 8 * k, xd + (L::kXHalf >> 4) + 2 * k, idesc, 1u);
+          tc_commit(L::kHB == 1 ? ae + 1 : ae);
+          tc_commit(xe);
           if (i == t.groups - 1) tc_commit(&dfull[buf]);
         }
         __syncwarp();
-        if (++s == NX) { s = 0; ph ^= 1; }
-        as += 2 / L::kHB;
-        if (as >= NA) { as -= NA; aph ^= 1; }
       }
       if (++buf == 2) { buf = 0; dph ^= 1; }
     }
@@ -454,20 +540,24 @@ __global__ void __launch_bounds__(kTfThreads, 1)
     const uint32_t ta = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + L::kACol;
     constexpr int kPerG = 2 / L::kHB;   // K blocks of a group
     const uint32_t N32 = static_cast<uint32_t>(args.N);
-    // scale and zero point of this thread's row (rows past N read the last one)
-    auto load_sz = [&](const TfUnit& t, int i, unsigned short& s, unsigned char& z) {   // of block i
-      uint32_t n = static_cast<uint32_t>(t.row0 + row);
-      n = n < N32 ? n : N32 - 1;
-      const uint32_t x = static_cast<uint32_t>(t.e * G + t.g0 + i / kPerG) * N32 + n;
-      s = reinterpret_cast<const unsigned short*>(args.scales)[x];
-      z = args.zeros[x];
+    // Scale and zero point of this thread's row (rows past N read the last one): index of those
+    // of K block i of a unit; the set's next block of the unit is a fixed step on.
+    const uint32_t sz_step = (kTfSets / kPerG) * N32;
+    auto sz_index = [&](const TfUnit& t, int i) {
+      const uint32_t n = static_cast<uint32_t>(t.row0 + row);
+      return static_cast<uint32_t>(t.e * G + t.g0 + i / kPerG) * N32 + (n < N32 ? n : N32 - 1);
+    };
+    uint32_t sz = 0;
+    auto load_sz = [&](unsigned short& s, unsigned char& z) {
+      s = reinterpret_cast<const unsigned short*>(args.scales)[sz];
+      z = args.zeros[sz];
     };
     unsigned short s_cur = 0, s_far = 0;   // of the block at hand; of the set's next block
     unsigned char z_cur = 0, z_far = 0;
     unsigned u = blockIdx.x;
     TfUnit t{}, tn{};       // the unit at hand and the CTA's next one
     if (u < units) t = tf_unit<BN>(u, args, tab, G);
-    int i = set;            // K block of the unit
+    int i = set;            // K block (A stage) of the unit
     int slot_i = 0;         // the ring's current slot is the unit's slot_i-th
     int ps = 0, as = set % NA;
     uint32_t ph = 0, aph = (set / NA) & 1;
@@ -493,7 +583,10 @@ __global__ void __launch_bounds__(kTfThreads, 1)
       u += gridDim.x;
       if (u < units) t = tf_unit<BN>(u, args, tab, G);
     }
-    if (u < units) load_sz(t, i, s_far, z_far);
+    if (u < units) {
+      sz = sz_index(t, i);
+      load_sz(s_far, z_far);
+    }
     while (u < units && ok) {
       // the set's next block: in this unit, or in the first later one that has it
       unsigned un = u;
@@ -502,7 +595,8 @@ __global__ void __launch_bounds__(kTfThreads, 1)
       s_cur = s_far;
       z_cur = z_far;
       if (same) {
-        load_sz(t, in, s_far, z_far);
+        sz += sz_step;
+        load_sz(s_far, z_far);
       } else {
         tn = t;
         while (un < units && in >= kPerG * tn.groups) {
@@ -510,7 +604,10 @@ __global__ void __launch_bounds__(kTfThreads, 1)
           un += gridDim.x;
           if (un < units) tn = tf_unit<BN>(un, args, tab, G);
         }
-        if (un < units) load_sz(tn, in, s_far, z_far);
+        if (un < units) {
+          sz = sz_index(tn, in);
+          load_sz(s_far, z_far);
+        }
       }
       {
         const int gi = i / kPerG % kPG, h = i % kPerG;   // group of the slot, half of the group
@@ -578,67 +675,31 @@ __global__ void __launch_bounds__(kTfThreads, 1)
   } else if (warp >= kTfEpiWarp0) {
     // ------------------------------------------------------------------ epilogue
     pdl_wait();
-    using A = act_t<kBf16>;
     const int half = (warp - kTfEpiWarp0) >> 2;
     const int row = 32 * (warp & 3) + lane;
-    const uint32_t td = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + L::kAccCol;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     int buf = 0;
     uint32_t ph = 0;
     for (unsigned u = blockIdx.x; u < units; u += gridDim.x) {
       const TfUnit t = tf_unit<BN>(u, args, tab, G);
       const int64_t n = t.row0 + row;
-      const int cols = t.cols;
-      const bool live = n < args.N && AWQ_IN_BOUNDS(t.m0 + cols <= args.M && t.e < args.E);
+      const bool live = n < args.N && AWQ_IN_BOUNDS(t.m0 + t.cols <= args.M && t.e < args.E);
       const float bias = live ? fused_bias<kBf16>(args.epi, t.e * args.N + n) : 0.0f;
+      const uint32_t td = tmem + lanes + L::kAccCol + buf * BN;
       if (!__all_sync(0xffffffffu, mbar_wait_lazy(&dfull[buf], ph))) break;
       tc_fence_after();
-#pragma unroll 1
-      for (int c0 = 16 * half; c0 < cols; c0 += 32) {   // the halves take alternate 16 columns
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(td + buf * BN + c0, v);
-        tmem_ld_wait();
-        const int nc = cols - c0 < 16 ? cols - c0 : 16;
-        if (args.factors != nullptr) {   // the tokens' factors (prepared activations)
-          const float* f = args.factors + t.m0 + c0;
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (j < nc) v[j] = __float_as_uint(__uint_as_float(v[j]) * f[j]);
+      if (args.k_splits > 1) {
+        partial_tile<kBf16>(args, t, n, live, half, lane, td);
+      } else {
+        switch (args.epi.act) {
+          case kActRelu: fused_tile<kBf16, kActRelu>(args, t, n, live, bias, half, lane, td); break;
+          case kActSilu: fused_tile<kBf16, kActSilu>(args, t, n, live, bias, half, lane, td); break;
+          case kActGelu: fused_tile<kBf16, kActGelu>(args, t, n, live, bias, half, lane, td); break;
+          case kActGeluTanh:
+            fused_tile<kBf16, kActGeluTanh>(args, t, n, live, bias, half, lane, td);
+            break;
+          default: fused_tile<kBf16, kActNone>(args, t, n, live, bias, half, lane, td);
         }
-        const int64_t y = static_cast<int64_t>(t.m0 + c0) * args.N + n;
-        if (live) {
-          A* Y = static_cast<A*>(args.Y);
-          if (args.k_splits > 1) {
-            float* p = args.partial + static_cast<int64_t>(t.ksplit) * args.M * args.N + y;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (j < nc) p[j * args.N] = __uint_as_float(v[j]);
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < 16; c += 8) {
-              const int64_t yc = y + c * args.N;
-              uint32_t w[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) w[j] = c ? v[8 + j] : v[j];
-              switch (args.epi.act) {
-                case kActRelu:
-                  fused_columns<kBf16, kActRelu>(args.epi, Y, yc, args.N, nc - c, bias, w);
-                  break;
-                case kActSilu:
-                  fused_columns<kBf16, kActSilu>(args.epi, Y, yc, args.N, nc - c, bias, w);
-                  break;
-                case kActGelu:
-                  fused_columns<kBf16, kActGelu>(args.epi, Y, yc, args.N, nc - c, bias, w);
-                  break;
-                case kActGeluTanh:
-                  fused_columns<kBf16, kActGeluTanh>(args.epi, Y, yc, args.N, nc - c, bias, w);
-                  break;
-                default:
-                  fused_columns<kBf16, kActNone>(args.epi, Y, yc, args.N, nc - c, bias, w);
-              }
-            }
-          }
-        }
-        __syncwarp();   // the next TMEM load is the whole warp's
       }
       tc_fence_before();
       __syncwarp();
