@@ -863,7 +863,8 @@ int tensor_bn(int64_t T, int64_t E) {
 // Which product kernel a call takes, from its shape alone, and the streaming kernel's variant.
 struct FusedPlan {
   enum Kind { kDecode, kStream, kTensor } kind;
-  int rb, xrows, slots;   // kStream
+  int rb, xrows, slots;   // kStream; split: each token as two rows of X
+  int split;
   int splits;             // kTensor: K slices, and where their partial sums start
   size_t prepared;
   size_t workspace;
@@ -887,6 +888,7 @@ awq_status launch_stream(const FusedPlan& plan, const void* X, const float* inv_
   constexpr int kRows = awq::kGemvRows * kRB;
   a.xrows = plan.xrows;
   a.slots = plan.slots;
+  a.split = plan.split;
   CUtensorMap tw;
   if (!make_tmap_2d(&tw, qweight, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.E * a.N, a.K * kBits / 32,
                     kRows, 32, true))
@@ -894,13 +896,14 @@ awq_status launch_stream(const FusedPlan& plan, const void* X, const float* inv_
   // X in the kernel's layout first, in the workspace
   const awq_status r = launch_pdl(
       awq::prepare_rows_kernel<kBf16, true>, dim3(static_cast<unsigned>(a.T)), awq::kPrepThreads, 0, st,
-      static_cast<const uint4*>(X), a.T, a.K, inv_s, a.offsets, a.E, L::kChunkG, L::kXChunk,
+      static_cast<const uint4*>(X), a.T, a.K, inv_s, a.offsets, a.E, L::kChunkG, L::kXChunk, a.split,
       static_cast<uint8_t*>(workspace));
   if (r != AWQ_OK) return r;
   a.xprep = static_cast<const uint8_t*>(workspace);
-  // at most this many tiles: T rows in blocks of xrows, one more for each expert with rows
-  const int64_t blocks = a.offsets == nullptr ? (a.T + a.xrows - 1) / a.xrows
-                                              : a.T / a.xrows + (a.T < a.E ? a.T : a.E);
+  // at most this many tiles: T rows in blocks, one more for each expert with rows
+  const int tokens = a.xrows >> a.split;
+  const int64_t blocks = a.offsets == nullptr ? (a.T + tokens - 1) / tokens
+                                              : a.T / tokens + (a.T < a.E ? a.T : a.E);
   const int64_t tiles = (a.N + kRows - 1) / kRows * blocks;
   const int smem = L::total(a.slots, a.xrows, a.E);
   const int64_t ctas = static_cast<int64_t>(num_sms()) * (smem <= kCoResidentSmem ? 2 : 1);
@@ -929,7 +932,7 @@ void plan_stream(FusedPlan& p, int64_t T, int64_t E, int64_t K) {
     if (p.slots >= 2) break;
   }
   const int64_t chunks = (K / awq::kGroup + L::kChunkG - 1) / L::kChunkG;
-  p.workspace = align256(static_cast<size_t>(T) * (chunks * L::kXChunk + sizeof(float)));
+  p.workspace = align256(static_cast<size_t>(T) * ((chunks * L::kXChunk << p.split) + sizeof(float)));
 }
 
 // The decode kernel (one launch, no workspace) for the shortest dense calls: at M = 1, 4 and 8 it
@@ -939,15 +942,20 @@ void plan_stream(FusedPlan& p, int64_t T, int64_t E, int64_t K) {
 // The streaming kernel up to 8 rows of an expert on average: 8 experts of [14336, 4096] with 64
 // rows took 80 us there and 100 on the tensor-core kernel, with 128 rows 138 (in blocks of 16
 // tokens) and 101.
-FusedPlan fused_plan(int64_t T, int64_t E, int64_t N, int64_t K, bool grouped) {
+// inv_s: the decode kernel rounds x * inv_s to 16 bits, so a call with it goes to the others; fp16
+// activations then take two rows each in the streaming kernel, which leaves it half the tokens.
+FusedPlan fused_plan(int64_t T, int64_t E, int64_t N, int64_t K, bool grouped, bool inv, bool bf16) {
   FusedPlan p{};
-  if (!grouped && (T <= 2 || (T <= 8 && N <= (int64_t{1} << 25) / K)) && gemv_stream_fits(T, N, K)) {
+  if (!grouped && !inv && (T <= 2 || (T <= 8 && N <= (int64_t{1} << 25) / K)) &&
+      gemv_stream_fits(T, N, K)) {
     p.kind = FusedPlan::kDecode;
     return p;
   }
-  if (T <= 8 * E) {
-    p.xrows = static_cast<int>(T < 8 ? T : 8);
-    const int64_t blocks = grouped ? T / p.xrows + (T < E ? T : E) : 1;
+  p.split = inv && !bf16 ? 1 : 0;
+  const int most = 8 >> p.split;   // tokens of a block
+  if (T <= most * E) {
+    p.xrows = static_cast<int>(T < most ? T : most) << p.split;
+    const int64_t blocks = grouped ? T / most + (T < E ? T : E) : 1;
     // 64 weight rows a tile read the tokens least often; 32 with few tokens (one token of two
     // experts [14336, 4096]: 18.7 us against 20.0), and fewer where there are too few tiles
     int rb = p.xrows <= 4 ? 2 : 4;
@@ -1006,6 +1014,16 @@ awq_status launch_tensor(const void* X, const uint32_t* qweight, const awq::Fuse
   }
 }
 
+// What any call of the shape may need, with inv_s or without, of either type.
+size_t fused_workspace(int64_t T, int64_t E, int64_t N, int64_t K, bool grouped) {
+  size_t most = 0;
+  for (int kind = 0; kind < 4; ++kind) {
+    const size_t w = fused_plan(T, E, N, K, grouped, (kind & 1) != 0, (kind & 2) != 0).workspace;
+    if (w > most) most = w;
+  }
+  return most;
+}
+
 // What the products with a fused epilogue share: argument checks past the shapes, and the
 // launch. E experts with N rows each; offsets NULL for one expert with every row of X.
 awq_status fused_gemm(const void* X, int64_t T, const int32_t* offsets, int64_t E,
@@ -1030,7 +1048,7 @@ awq_status fused_gemm(const void* X, int64_t T, const int32_t* offsets, int64_t 
   if (E * N > kMaxDim || E * (K / awq::kGroup) > kMaxDim / N) return AWQ_ERR_INVALID_ARG;
   const bool bf16 = (flags & AWQ_GEMM_BF16) != 0;
   const awq::FusedEpi epi{bias, mul, residual, act};
-  const FusedPlan plan = fused_plan(T, E, N, K, offsets != nullptr);
+  const FusedPlan plan = fused_plan(T, E, N, K, offsets != nullptr, inv_s != nullptr, bf16);
   if (plan.workspace > 0 && (!workspace || ws_bytes < plan.workspace || !aligned16(workspace)))
     return AWQ_ERR_WORKSPACE;
   if (plan.kind == FusedPlan::kDecode)
@@ -1072,7 +1090,7 @@ awq_status fused_gemm(const void* X, int64_t T, const int32_t* offsets, int64_t 
   if (bf16) {
     r = launch_pdl(awq::prepare_rows_kernel<true, false>, dim3(static_cast<unsigned>(T)),
                    awq::kPrepThreads, 0, st, static_cast<const uint4*>(X), static_cast<int>(T), K,
-                   inv_s, offsets, static_cast<int>(E), 1, 0, static_cast<uint8_t*>(workspace));
+                   inv_s, offsets, static_cast<int>(E), 1, 0, 0, static_cast<uint8_t*>(workspace));
     if (r != AWQ_OK) return r;
     X = workspace;
     args.factors = reinterpret_cast<const float*>(static_cast<uint8_t*>(workspace) + T * K * 2);
@@ -1134,7 +1152,7 @@ extern "C" {
 size_t awq_gemm_epilogue_workspace_size(int64_t M, int64_t N, int64_t K, int bits) {
   if (M <= 0 || K <= 0 || N <= 0) return 0;
   (void)bits;
-  return fused_plan(M, 1, N, K, false).workspace;
+  return fused_workspace(M, 1, N, K, false);
 }
 
 awq_status awq_gemm_w4a16_epilogue(const awq_f16* X, int64_t M, const uint32_t* qweight,
@@ -1152,7 +1170,7 @@ size_t awq_gemm_grouped_workspace_size(int64_t T, int64_t E, int64_t N, int64_t 
   if (T <= 0 || E <= 0 || K <= 0 || N <= 0) return 0;
   (void)bits;
   if (E > awq::kMaxExperts) return 0;
-  return fused_plan(T, E, N, K, true).workspace;
+  return fused_workspace(T, E, N, K, true);
 }
 
 awq_status awq_gemm_w4a16_grouped(const awq_f16* X, int64_t T, const int32_t* offsets, int64_t E,

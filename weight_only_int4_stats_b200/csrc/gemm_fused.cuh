@@ -24,8 +24,9 @@
 // fit beside four A stages and a tile's epilogue always overlaps the next tile's products. (A
 // set's turn comes round after four A stages, and a barrier's parity tells only neighbouring
 // phases apart: a stage must not come round sooner, so kNA >= the sets.)
-// Waiting on a barrier whose phase is already complete still takes about 100 cycles, so the waits
-// of one step are polled together, and the MMA issuer takes a whole group a step.
+// Waiting on a barrier whose phase is already complete still takes about 100 cycles, so a step is as
+// long as it can be: the MMA issuer takes a whole group. (Polling the next group's barriers ahead
+// of a group's MMAs was slower: [14336, 4096] with 4096 tokens 442 us against 428.)
 // The products are fp16: bf16 activations come from prepare_rows_kernel as fp16, scaled by a power
 // of two per row (with inv_s already in), and the epilogue takes the row's factor off. bf16
 // weights would need (q - z) * scale in two bf16 parts to be rounded only once (19 operations a
@@ -442,19 +443,11 @@ __global__ void __launch_bounds__(kTfThreads, 1)
     // The whole warp walks the loop, so that what the instructions take (descriptors, TMEM
     // addresses) is the same in every lane and lives in uniform registers; one elected lane
     // issues. (A loop that only lane 0 ran issued one MMA in about 80 cycles, whatever its N.)
-    // The next group's barriers are polled before this group's MMAs are issued, so that the
-    // polls' latency passes behind them.
     const bool leader = elect_one();
     const uint64_t xd0 = sw128_kmajor_desc(smem_u32(smem));
     int s = 0, as = 0, buf = 0;
     uint32_t ph = 0, aph = 0, dph = 0;
-    bool ok = true, ready = false;
-    const auto poll = [&]() {   // of stages s, as (kHB = 1: as is even, and as + 1)
-      const bool r0 = mbar_test_wait(&xfull[s], ph);
-      const bool r1 = mbar_test_wait(&afull[as], aph);
-      const bool r2 = L::kHB == 2 || mbar_test_wait(&afull[as + 1], aph);
-      return r0 && r1 && r2;
-    };
+    bool ok = true;
     for (unsigned u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const TfUnit t = tf_unit<BN>(u, args, tab, G);
       // a tile multiplies only the tokens it has (N goes in steps of 16): the rest of its BN rows
@@ -463,12 +456,10 @@ __global__ void __launch_bounds__(kTfThreads, 1)
       const uint32_t d = tmem + L::kAccCol + buf * BN;
       ok = __all_sync(0xffffffffu, mbar_wait(&dempty[buf], dph ^ 1));   // the epilogue has read it
       for (int i = 0; i < t.groups && ok; ++i) {
-        if (!__all_sync(0xffffffffu, ready)) {
-          ok = mbar_wait(&xfull[s], ph) && mbar_wait(&afull[as], aph) &&
-               (L::kHB == 2 || mbar_wait(&afull[as + 1], aph));
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-        }
+        ok = mbar_wait(&xfull[s], ph) && mbar_wait(&afull[as], aph) &&
+             (L::kHB == 2 || mbar_wait(&afull[as + 1], aph));   // (kHB = 1: as is even)
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         tc_fence_after();
         const uint64_t xd = xd0 + static_cast<uint64_t>(s * (L::kXBytes >> 4));
         const uint32_t a = tmem + L::kACol + as * L::kACols;
@@ -477,7 +468,6 @@ __global__ void __launch_bounds__(kTfThreads, 1)
         if (++s == NX) { s = 0; ph ^= 1; }
         as += 2 / L::kHB;
         if (as == NA) { as = 0; aph ^= 1; }
-        ready = poll();
         if (leader) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)   // 16 k each: 8 columns of A, 32 bytes of X

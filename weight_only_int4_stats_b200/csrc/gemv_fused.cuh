@@ -15,7 +15,9 @@
 // That kernel also makes fp16 of bf16 activations (scaled by a power of two per row, so nothing
 // a product could notice is lost), multiplies by inv_s in fp32 with one rounding, and lays the
 // rows out as the B fragments are read.
-//  * Work is a list of tiles (expert, block of up to xrows <= 8 tokens, 16 kRB weight rows)
+// fp16 activations with inv_s come as two rows, x' = hi + lo (22 bits), whose products are added at
+// the end, since one rounded row would err as much as the output's own rounding does.
+//  * Work is a list of tiles (expert, block of up to 8 rows of X, 16 kRB weight rows)
 //    that each CTA takes a contiguous range of; the experts' row counts come from the device.
 //  * The tokens come through the same ring as the weights, chunk by chunk, one bulk copy per
 //    row, so no CTA waits to stage X and X may be of any length.
@@ -45,7 +47,8 @@ struct StreamArgs {
   FusedEpi epi;
   void* Y;
   int slots;              // ring depth
-  int xrows;              // tokens of a block (at most 8): token rows of a slot
+  int xrows;              // rows of X of a block (at most 8) and of a slot
+  int split;              // 1: a token is two rows of X, the parts of x = hi + lo
 };
 
 // Shared memory from a 1024-byte aligned base: per slot the packed codes, then the token rows;
@@ -184,6 +187,7 @@ __global__ void __launch_bounds__(kG4Threads, 2) stream_fused_kernel(
   const int G = Ki / kGroup;
   const int C = (G + L::kChunkG - 1) / L::kChunkG;
   const int ntiles = static_cast<int>((a.N + kRows - 1) / kRows);
+  const int tokens = a.xrows >> a.split;   // of a block
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -196,7 +200,7 @@ __global__ void __launch_bounds__(kG4Threads, 2) stream_fused_kernel(
   // The kernel before this one is prepare_rows_kernel, which lets this one start only after its
   // own predecessors have completed: offsets, weights and scales are there, and only what it
   // writes has to be waited for.
-  if (warp == 0) build_group_table(off, tile, a.offsets, a.E, a.T, a.xrows);
+  if (warp == 0) build_group_table(off, tile, a.offsets, a.E, a.T, tokens);
   __syncthreads();
   const int64_t total = static_cast<int64_t>(tile[a.E]) * ntiles;
   const int64_t P = gridDim.x, bx = blockIdx.x;
@@ -212,17 +216,18 @@ __global__ void __launch_bounds__(kG4Threads, 2) stream_fused_kernel(
     int64_t idx = t0;
     auto weights = [&]() {   // lane 0: the unit's packed codes
       uint8_t* wb = smem + slot * slot_bytes;
-      mbar_arrive_expect_tx(&full[slot], kWTx + static_cast<uint32_t>(cur.rows) * L::kXChunk);
+      mbar_arrive_expect_tx(&full[slot], kWTx + static_cast<uint32_t>(cur.rows << a.split) * L::kXChunk);
       const int32_t row = static_cast<int32_t>(cur.e * a.N + static_cast<int64_t>(cur.nt) * kRows);
 #pragma unroll
       for (int b = 0; b < kBoxes; ++b)
         tma_load_2d(wb + b * kBox, &tmap_w, &full[slot], chunk * kRowW + b * 32, row);
     };
-    auto tokens = [&]() {   // lane m: token row m's chunk
-      if (lane < cur.rows && AWQ_IN_BOUNDS(cur.m0 + lane < a.T && lane < a.xrows))
+    auto activations = [&]() {   // lane m: row m's chunk
+      const int row = (cur.m0 << a.split) + lane;
+      if (lane < cur.rows << a.split && AWQ_IN_BOUNDS(row < a.T << a.split && lane < a.xrows))
         bulk_load_1d(smem + slot * slot_bytes + L::kWBytes + lane * L::kXChunk,
-                     a.xprep + ((static_cast<int64_t>(cur.m0) + lane) * C + chunk) * L::kXChunk,
-                     L::kXChunk, &full[slot]);
+                     a.xprep + (static_cast<int64_t>(row) * C + chunk) * L::kXChunk, L::kXChunk,
+                     &full[slot]);
     };
     auto prefetch_sz = [&]() {   // scales (lanes 0..15) and zero points (16..31) of the unit
       const int g = chunk * L::kChunkG + (lane & 15);
@@ -238,10 +243,10 @@ __global__ void __launch_bounds__(kG4Threads, 2) stream_fused_kernel(
       if (++slot == S) { slot = 0; ph ^= 1; }
       if (++chunk == C) {
         chunk = 0;
-        if (++idx < t1) next_tile(cur, off, tile, a.E, idx, ntiles, a.xrows);
+        if (++idx < t1) next_tile(cur, off, tile, a.E, idx, ntiles, tokens);
       }
     };
-    if (t0 < t1) tile_at(cur, off, tile, a.E, idx, ntiles, a.xrows);
+    if (t0 < t1) tile_at(cur, off, tile, a.E, idx, ntiles, tokens);
     int64_t u = 0;
     const int64_t n_early = units < S ? units : S;
     for (; u < n_early; ++u) {   // the weights of the (empty) ring's units
@@ -254,16 +259,16 @@ __global__ void __launch_bounds__(kG4Threads, 2) stream_fused_kernel(
     slot = chunk = 0;
     ph = 0;
     idx = t0;
-    if (t0 < t1) tile_at(cur, off, tile, a.E, idx, ntiles, a.xrows);
-    for (int64_t v = 0; v < n_early; ++v) {   // and their tokens
-      tokens();
+    if (t0 < t1) tile_at(cur, off, tile, a.E, idx, ntiles, tokens);
+    for (int64_t v = 0; v < n_early; ++v) {   // and their activations
+      activations();
       advance();
     }
     for (; u < units; ++u) {
       if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ph ^ 1))) break;
       if (lane == 0) weights();
       __syncwarp();   // the transaction count is set before any of the copies can complete it
-      tokens();
+      activations();
       prefetch_sz();
       advance();
     }
@@ -272,7 +277,7 @@ __global__ void __launch_bounds__(kG4Threads, 2) stream_fused_kernel(
 
   // ------------------------------------------------------------------ consumers
   const float* factors = reinterpret_cast<const float*>(
-      a.xprep + static_cast<int64_t>(a.T) * C * L::kXChunk);
+      a.xprep + static_cast<int64_t>(a.T << a.split) * C * L::kXChunk);
   const int r = lane >> 2, c = lane & 3;
   const int rw = (r >> 1) + 4 * (r & 1);   // weight row of the MMA's row r (see gemv.cuh)
   const int rb = warp % kRB;               // this warp's row block, and its kGW groups
@@ -337,7 +342,7 @@ __global__ void __launch_bounds__(kG4Threads, 2) stream_fused_kernel(
   TileCursor nxt{};
   Raw raw, raw_next;
   if (t0 < t1) {
-    tile_at(cur, off, tile, a.E, idx, ntiles, a.xrows);
+    tile_at(cur, off, tile, a.E, idx, ntiles, tokens);
     nxt = cur;
     sz_tile(cur);
     load_sz(raw, 0);
@@ -349,7 +354,7 @@ __global__ void __launch_bounds__(kG4Threads, 2) stream_fused_kernel(
     const bool last = chunk == C - 1;
     if (u + 1 < units) {
       if (last) {
-        next_tile(nxt, off, tile, a.E, idx + 1, ntiles, a.xrows);
+        next_tile(nxt, off, tile, a.E, idx + 1, ntiles, tokens);
         sz_tile(nxt);
       }
       load_sz(raw_next, last ? 0 : chunk + 1);
@@ -357,7 +362,9 @@ __global__ void __launch_bounds__(kG4Threads, 2) stream_fused_kernel(
     // what the epilogue reads of the outputs that this lane stores, ahead of the last unit
     const bool finisher = last && warp < kRB;
     FusedIn<kBf16> fin;
-    float fs[2];        // the factors of the lane's tokens
+    // the lane's tokens are 2c and 2c + 1 of the block, or c with both parts
+    const int fm = a.split ? c : 2 * c;
+    float fs[2];        // their factors
     const int64_t fn = static_cast<int64_t>(cur.nt) * kRows + ra;
     FusedEpi epi = a.epi;
     if (finisher) {
@@ -365,9 +372,9 @@ __global__ void __launch_bounds__(kG4Threads, 2) stream_fused_kernel(
       const int64_t y = cur.m0 * a.N;
       if (epi.mul != nullptr) epi.mul = static_cast<const A*>(epi.mul) + y;
       if (epi.residual != nullptr) epi.residual = static_cast<const A*>(epi.residual) + y;
-      fin.load(epi, fn, 2 * c, a.N, cur.rows);
+      fin.load(epi, fn, fm, a.N, cur.rows);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) fs[i] = 2 * c + i < cur.rows ? factors[cur.m0 + 2 * c + i] : 0.0f;
+      for (int i = 0; i < 2; ++i) fs[i] = fm + i < cur.rows ? factors[cur.m0 + fm + i] : 0.0f;
     }
     ok = __all_sync(0xffffffffu, ok && mbar_wait(&full[slot], ph));
     uint32_t sz[kGW / 2];   // (scale, zero point) of this unit as fp16 pairs
@@ -447,16 +454,24 @@ __global__ void __launch_bounds__(kG4Threads, 2) stream_fused_kernel(
       }
       named_bar_sync(1 + rb, kG4Warps / kRB * 32);   // the warps of the row block
       if (finisher && ok) {
+        float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float v = 0.0f;
+          v[i] = 0.0f;
 #pragma unroll
-          for (int w = 0; w < kG4Warps / kRB; ++w) v += rd[((w * kRB + rb) * 4 + i) * 32 + lane];
-          const int m = 2 * c + (i & 1);
+          for (int w = 0; w < kG4Warps / kRB; ++w) v[i] += rd[((w * kRB + rb) * 4 + i) * 32 + lane];
+        }
+        if (a.split) {
+          v[0] += v[1];
+          v[2] += v[3];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int m = fm + (i & 1);
           const int64_t n = fn + 8 * (i >> 1);
-          if (m < cur.rows && n < a.N && AWQ_IN_BOUNDS(cur.m0 + m < a.T))
+          if (m < cur.rows && n < a.N && !(a.split && (i & 1)) && AWQ_IN_BOUNDS(cur.m0 + m < a.T))
             static_cast<A*>(a.Y)[(static_cast<int64_t>(cur.m0) + m) * a.N + n] =
-                float_to_act<kBf16>(fin.apply(epi, v * fs[i & 1], i));
+                float_to_act<kBf16>(fin.apply(epi, v[i] * fs[i & 1], i));
         }
       }
       chunk = 0;

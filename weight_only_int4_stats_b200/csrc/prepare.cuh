@@ -10,7 +10,8 @@ namespace awq {
 // become fp16 without a loss that a product could notice, and nothing overflows. One CTA per row.
 //  * kFragments, for the streaming kernel (gemv_fused.cuh): chunks of chunk_groups groups, each
 //    group [8-k chunk j][32-k quarter c] of 8 values as the MMA fragments are read, then the
-//    groups' sums of x' times 2^-24; the factor is times 2^24 (the codes come in as q 2^-24).
+//    groups' sums of x' times 2^-24; the factor is times 2^24 (the codes come in as q 2^-24). With
+//    split = 1 a row is two: x' rounded, then the rounding's remainder, rounded.
 //  * else plain rows [T, K], for the tensor-core kernel (gemm_fused.cuh).
 // The factors [T] follow the rows.
 constexpr int kPrepThreads = 256;
@@ -37,7 +38,7 @@ __device__ __forceinline__ void prep_load(float (&f)[8], const uint4* X, const f
 template <bool kBf16, bool kFragments>
 __global__ void __launch_bounds__(kPrepThreads) prepare_rows_kernel(
     const uint4* __restrict__ X, int T, int64_t K, const float* __restrict__ inv_s,
-    const int* __restrict__ offsets, int E, int chunk_groups, int chunk_bytes,
+    const int* __restrict__ offsets, int E, int chunk_groups, int chunk_bytes, int split,
     uint8_t* __restrict__ out) {
   pdl_wait();
   pdl_launch_dependents();
@@ -78,40 +79,49 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_rows_kernel(
   int p = finite && big > 0.0f ? 14 - (static_cast<int>(__float_as_uint(big) >> 23) - 127) : 0;
   p = p > 100 ? 100 : p < -100 ? -100 : p;
   const float up = __uint_as_float(static_cast<uint32_t>(127 + p) << 23);
-  uint8_t* base = out + static_cast<int64_t>(row) * chunks * chunk_bytes;
+  const int64_t row_bytes = static_cast<int64_t>(chunks) * chunk_bytes;
+  uint8_t* base = out + (static_cast<int64_t>(row) << split) * row_bytes;
   // whole groups (16 lanes each) per iteration: lanes past the row's end take part in the sums
   for (int i = tid; i < (nch + 31) / 32 * 32; i += kPrepThreads) {
     float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     const bool live = i < nch;
     if (live) prep_load<kBf16>(f, X, inv_s, i);
-    uint32_t v[4];
-    float sum = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = float2_to_act2<false>(f[2 * e] * up, f[2 * e + 1] * up);
-      const float2 g = act2_to_float2<false>(v[e]);
-      sum += g.x + g.y;
-    }
-    if (kFragments)
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const int g = i >> 4, ch = i & 15;   // 8-k chunk ch of the group: quarter ch / 4, j = ch % 4
     const int gl = g % chunk_groups;
     uint8_t* c = base + static_cast<int64_t>(g / chunk_groups) * chunk_bytes;
-    if (!kFragments) {
-      if (live && AWQ_IN_BOUNDS(row < T))
-        reinterpret_cast<uint4*>(out)[static_cast<int64_t>(row) * nch + i] =
-            make_uint4(v[0], v[1], v[2], v[3]);
-    } else if (live && AWQ_IN_BOUNDS(row < T)) {
-      *reinterpret_cast<uint4*>(c + gl * 256 + (ch & 3) * 64 + (ch >> 2) * 16) =
-          make_uint4(v[0], v[2], v[1], v[3]);   // the pairs of the two MMAs
-      if (ch == 0)
-        *reinterpret_cast<float*>(c + chunk_groups * 256 + gl * 4) = sum * 5.9604644775390625e-8f;
+    for (int part = 0; part <= split; ++part) {   // the rounded value, then what it left
+      uint32_t v[4];
+      float sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x0 = part == 0 ? f[2 * e] * up : f[2 * e];
+        const float x1 = part == 0 ? f[2 * e + 1] * up : f[2 * e + 1];
+        v[e] = float2_to_act2<false>(x0, x1);
+        const float2 h = act2_to_float2<false>(v[e]);
+        sum += h.x + h.y;
+        f[2 * e] = x0 - h.x;
+        f[2 * e + 1] = x1 - h.y;
+      }
+      if (!kFragments) {
+        if (live && AWQ_IN_BOUNDS(row < T))
+          reinterpret_cast<uint4*>(out)[static_cast<int64_t>(row) * nch + i] =
+              make_uint4(v[0], v[1], v[2], v[3]);
+        break;
+      }
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      uint8_t* cp = c + part * row_bytes;
+      if (live && AWQ_IN_BOUNDS(row < T)) {
+        *reinterpret_cast<uint4*>(cp + gl * 256 + (ch & 3) * 64 + (ch >> 2) * 16) =
+            make_uint4(v[0], v[2], v[1], v[3]);   // the pairs of the two MMAs
+        if (ch == 0)
+          *reinterpret_cast<float*>(cp + chunk_groups * 256 + gl * 4) = sum * 5.9604644775390625e-8f;
+      }
     }
   }
   if (tid == 0) {
     const int64_t rows_bytes =
-        kFragments ? static_cast<int64_t>(T) * chunks * chunk_bytes : static_cast<int64_t>(T) * K * 2;
+        kFragments ? (static_cast<int64_t>(T) << split) * row_bytes : static_cast<int64_t>(T) * K * 2;
     reinterpret_cast<float*>(out + rows_bytes)[row] =
         __uint_as_float(static_cast<uint32_t>(127 - p) << 23) * (kFragments ? 16777216.0f : 1.0f);
   }
