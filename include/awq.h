@@ -246,15 +246,21 @@ AWQ_API awq_status awq_gemm_w4a16(const awq_f16* X, int64_t M, const uint32_t* q
  *     GELU_TANH v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2.
  * mul or residual may be Y itself (each output is read before it is written, by the same
  * thread); apart from that Y overlaps no input. The other arguments, the flags and the
- * no-ops are awq_gemm_w4a16's. Activations scaled by inv_s are rounded to 16 bits in the
- * decode kernel; the tensor-core kernel rounds (q - z) * scale * inv_s[k] once, from fp32.
- * workspace: at least awq_gemm_epilogue_workspace_size(M, N, K, bits) bytes. */
+ * no-ops are awq_gemm_w4a16's.
+ * Roundings before the output's: up to 8 rows none, with inv_s in fp16 too (x * inv_s is held in
+ * two fp16 parts), while bf16 activations times inv_s are rounded once to fp16's 11 bits, scaled
+ * by a power of two per row; more rows take the weights as fp16, (q - z) * scale rounded once
+ * (times inv_s[k] before that rounding, for fp16 activations). A row of X that holds an infinity
+ * or a NaN gives infinities or NaN, which of the two is not specified; other rows do not notice.
+ * workspace: at least awq_gemm_epilogue_workspace_size(M, N, K, bits, inv_s != NULL, flags)
+ * bytes. */
 #define AWQ_ACT_NONE 0
 #define AWQ_ACT_RELU 1
 #define AWQ_ACT_SILU 2
 #define AWQ_ACT_GELU 3
 #define AWQ_ACT_GELU_TANH 4
-AWQ_API size_t awq_gemm_epilogue_workspace_size(int64_t M, int64_t N, int64_t K, int bits);
+AWQ_API size_t awq_gemm_epilogue_workspace_size(int64_t M, int64_t N, int64_t K, int bits,
+                                                int with_inv_s, unsigned flags);
 AWQ_API awq_status awq_gemm_w4a16_epilogue(
     const awq_f16* X, int64_t M, const uint32_t* qweight, const awq_f16* scales,
     const uint8_t* zeros, int64_t N, int64_t K, int bits, int group, const float* inv_s,
@@ -274,8 +280,10 @@ AWQ_API awq_status awq_gemm_w4a16_epilogue(
  * awq_gemm_w4a16_grouped: awq_gemm_w4a16_epilogue's product, each row against its expert's
  * packed weight: qweight [E, N, K/8] (or [E, N, 3K/32]), scales [E, K/128, N], zeros
  * [E, K/128, N], inv_s NULL or [E, K], bias NULL or [E, N]; mul, residual, Y [T, N]. Only the
- * weights of experts with rows are read. E * N and E * N * K / 128 must be below 2^31. workspace: at least awq_gemm_grouped_workspace_size(T, E, N, K, bits) bytes. */
-AWQ_API size_t awq_gemm_grouped_workspace_size(int64_t T, int64_t E, int64_t N, int64_t K, int bits);
+ * weights of experts with rows are read. E * N and E * N * K / 128 must be below 2^31. workspace: at least
+ * awq_gemm_grouped_workspace_size(T, E, N, K, bits, inv_s != NULL, flags) bytes. */
+AWQ_API size_t awq_gemm_grouped_workspace_size(int64_t T, int64_t E, int64_t N, int64_t K, int bits,
+                                               int with_inv_s, unsigned flags);
 AWQ_API awq_status awq_gemm_w4a16_grouped(
     const awq_f16* X, int64_t T, const int32_t* offsets, int64_t E, const uint32_t* qweight,
     const awq_f16* scales, const uint8_t* zeros, int64_t N, int64_t K, int bits, int group,

@@ -59,7 +59,7 @@ def test_nothing_to_do(L):
 
 def test_workspace_missing_or_small(L):
     M, N, K = 64, 4096, 4096
-    need = L.awq_gemm_epilogue_workspace_size(M, N, K, 4)
+    need = L.awq_gemm_epilogue_workspace_size(M, N, K, 4, 0, 0)
     if need:
         assert epilogue(L, M=M, N=N, K=K, ws=None, n=0) == WORKSPACE
         assert epilogue(L, M=M, N=N, K=K, n=need - 1) == WORKSPACE

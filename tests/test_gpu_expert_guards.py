@@ -32,7 +32,7 @@ def test_epilogue_guarded(L, M, N, K, bits, inv):  # noqa: F811
     g = {k: Guarded(v.nbytes, v) for k, v in
          dict(x=X, q=qw, sc=sc, z=z, mul=mul, res=res, bias=bias, s=s).items()}
     y = Guarded(2 * M * N)
-    need = L.awq_gemm_epilogue_workspace_size(M, N, K, bits)
+    need = L.awq_gemm_epilogue_workspace_size(M, N, K, bits, inv, 0)
     ws = Guarded(need) if need else None
     for flags in (0, 1):
         _ok(L, L.awq_gemm_w4a16_epilogue(
@@ -62,7 +62,7 @@ def test_grouped_guarded(L, counts, N, K, bits):  # noqa: F811
     X, s = half(rng, T, K), rng.uniform(0.5, 2.0, (E, K)).astype(np.float32)
     g = {k: Guarded(v.nbytes, v) for k, v in dict(x=X, o=off, q=qw, sc=sc, z=z, s=s).items()}
     y = Guarded(2 * T * N, np.full(T * N, 7, np.float16))
-    need = L.awq_gemm_grouped_workspace_size(T, E, N, K, bits)
+    need = L.awq_gemm_grouped_workspace_size(T, E, N, K, bits, 1, 0)
     ws = Guarded(need) if need else None
     _ok(L, L.awq_gemm_w4a16_grouped(g["x"].ptr, T, g["o"].ptr, E, g["q"].ptr, g["sc"].ptr, g["z"].ptr,
                                     N, K, bits, 128, g["s"].ptr, None, 0, None, None, 0, y.ptr,

@@ -67,10 +67,10 @@ def load_library(path: str) -> ctypes.CDLL:
         "awq_silu_mul_gemm": (I32, [P, I64, P, P, I64, I64, P, P]),
         "awq_gemm_w4a16": (I32, [P, I64, P, P, P, I64, I64, I32, I32, P, ctypes.c_uint, P,
                                  P, SZ, P]),
-        "awq_gemm_epilogue_workspace_size": (SZ, [I64, I64, I64, I32]),
+        "awq_gemm_epilogue_workspace_size": (SZ, [I64, I64, I64, I32, I32, ctypes.c_uint]),
         "awq_gemm_w4a16_epilogue": (I32, [P, I64, P, P, P, I64, I64, I32, I32, P, P, I32, P, P,
                                           ctypes.c_uint, P, P, SZ, P]),
-        "awq_gemm_grouped_workspace_size": (SZ, [I64, I64, I64, I64, I32]),
+        "awq_gemm_grouped_workspace_size": (SZ, [I64, I64, I64, I64, I32, I32, ctypes.c_uint]),
         "awq_gemm_w4a16_grouped": (I32, [P, I64, P, I64, P, P, P, I64, I64, I32, I32, P, P, I32,
                                          P, P, ctypes.c_uint, P, P, SZ, P]),
         "awq_act_stats_grouped_workspace_size": (SZ, [I64, I64, I64]),
@@ -336,7 +336,7 @@ def _call(fn, index, stream, need, workspace, args):
     if need is not None:
         ws = workspace
         if ws is None and need > 0:
-            ws = _new(need, torch.uint8, torch.device("cuda", index), stream)
+            ws = _new(need, torch.uint8, index, stream)
         if ws is None:
             args += (None, 0)
         else:
@@ -373,16 +373,18 @@ def awq_gemm_w4a16_epilogue(X: torch.Tensor, qweight: torch.Tensor, scales: torc
     awq_gemm_w4a16."""
     dev, t, M = X.get_device(), X.dtype, X.shape[0]
     x, G = _activations(X, K, dev), K // GROUP
+    flags = (WEIGHTS_READY if weights_ready else 0) | (BF16 if t is torch.bfloat16 else 0)
     Y = _new((M, N), t, X.device, stream) if out is None else out
     _call("awq_gemm_w4a16_epilogue", dev, stream,
-          _workspace_bytes(lib(), "awq_gemm_epilogue_workspace_size", M, N, K, bits), workspace,
+          _workspace_bytes(lib(), "awq_gemm_epilogue_workspace_size", M, N, K, bits,
+                           inv_s is not None, flags), workspace,
           (x, M, _arg(qweight, torch.int32, (N, packed_words_per_row(K, bits)), dev, "qweight"),
            _arg(scales, torch.float16, (G, N), dev, "scales"),
            _arg(zeros, torch.uint8, (G, N), dev, "zeros"), N, K, bits, group,
            _arg(inv_s, torch.float32, (K,), dev, "inv_s"), _arg(bias, t, (N,), dev, "bias"),
            _act(act), _arg(mul, t, (M, N), dev, "mul"),
            _arg(residual, t, (M, N), dev, "residual"),
-           (WEIGHTS_READY if weights_ready else 0) | (BF16 if t is torch.bfloat16 else 0),
+           flags,
            _arg(Y, t, (M, N), dev, "out")))
     return Y
 
@@ -404,9 +406,11 @@ def awq_gemm_w4a16_grouped(X: torch.Tensor, offsets: torch.Tensor, qweight: torc
     (undefined without it)."""
     dev, t, T, E = X.get_device(), X.dtype, X.shape[0], offsets.numel() - 1
     x, G = _activations(X, K, dev), K // GROUP
+    flags = (WEIGHTS_READY if weights_ready else 0) | (BF16 if t is torch.bfloat16 else 0)
     Y = _new((T, N), t, X.device, stream) if out is None else out
     _call("awq_gemm_w4a16_grouped", dev, stream,
-          _workspace_bytes(lib(), "awq_gemm_grouped_workspace_size", T, E, N, K, bits), workspace,
+          _workspace_bytes(lib(), "awq_gemm_grouped_workspace_size", T, E, N, K, bits,
+                           inv_s is not None, flags), workspace,
           (x, T, _arg(offsets, torch.int32, (E + 1,), dev, "offsets"), E,
            _arg(qweight, torch.int32, (E, N, packed_words_per_row(K, bits)), dev, "qweight"),
            _arg(scales, torch.float16, (E, G, N), dev, "scales"),
@@ -414,7 +418,7 @@ def awq_gemm_w4a16_grouped(X: torch.Tensor, offsets: torch.Tensor, qweight: torc
            _arg(inv_s, torch.float32, (E, K), dev, "inv_s"),
            _arg(bias, t, (E, N), dev, "bias"), _act(act), _arg(mul, t, (T, N), dev, "mul"),
            _arg(residual, t, (T, N), dev, "residual"),
-           (WEIGHTS_READY if weights_ready else 0) | (BF16 if t is torch.bfloat16 else 0),
+           flags,
            _arg(Y, t, (T, N), dev, "out")))
     return Y
 

@@ -284,10 +284,12 @@ awq_status launch_gemv_stream_m(const void* x, int64_t M, const uint32_t* qweigh
   if (M == 1)
     return launch_gemv_stream_t<1, true, kBf16, kBits, kFused>(x, M, qweight, scales, zeros, N, K,
                                                                inv_s, flags, y, st, epi);
-  if (M <= 8)
-    return launch_gemv_stream_t<1, false, kBf16, kBits, kFused>(x, M, qweight, scales, zeros, N, K,
-                                                                inv_s, flags, y, st, epi);
-  return launch_gemv_stream_t<2, false, kBf16, kBits, kFused>(x, M, qweight, scales, zeros, N, K,
+  if constexpr (!kFused) {   // (the fused calls have at most 8 tokens: see fused_plan)
+    if (M > 8)
+      return launch_gemv_stream_t<2, false, kBf16, kBits, false>(x, M, qweight, scales, zeros, N, K,
+                                                                 inv_s, flags, y, st, epi);
+  }
+  return launch_gemv_stream_t<1, false, kBf16, kBits, kFused>(x, M, qweight, scales, zeros, N, K,
                                                               inv_s, flags, y, st, epi);
 }
 
@@ -967,7 +969,7 @@ FusedPlan fused_plan(int64_t T, int64_t E, int64_t N, int64_t K, bool grouped, b
   }
   p.kind = FusedPlan::kTensor;
   // prepared activations (bf16) and their factors, then the partial sums of K slices
-  p.prepared = align256(static_cast<size_t>(T) * (2 * K + sizeof(float)));
+  p.prepared = bf16 ? align256(static_cast<size_t>(T) * (2 * K + sizeof(float))) : 0;
   p.splits = grouped ? 1 : splitk_for(T, N, K, tensor_bn(T, 1));
   p.workspace = p.prepared +
                 (p.splits > 1 ? align256(static_cast<size_t>(p.splits) * T * N * sizeof(float)) : 0);
@@ -1012,16 +1014,6 @@ awq_status launch_tensor(const void* X, const uint32_t* qweight, const awq::Fuse
     case 128: return launch_tensor_bn<128, kBf16, kBits, kInv>(X, qweight, a, early, st);
     default: return launch_tensor_bn<192, kBf16, kBits, kInv>(X, qweight, a, early, st);
   }
-}
-
-// What any call of the shape may need, with inv_s or without, of either type.
-size_t fused_workspace(int64_t T, int64_t E, int64_t N, int64_t K, bool grouped) {
-  size_t most = 0;
-  for (int kind = 0; kind < 4; ++kind) {
-    const size_t w = fused_plan(T, E, N, K, grouped, (kind & 1) != 0, (kind & 2) != 0).workspace;
-    if (w > most) most = w;
-  }
-  return most;
 }
 
 // What the products with a fused epilogue share: argument checks past the shapes, and the
@@ -1149,10 +1141,11 @@ bool bad_groups(int64_t E, const int32_t* offsets) {
 
 extern "C" {
 
-size_t awq_gemm_epilogue_workspace_size(int64_t M, int64_t N, int64_t K, int bits) {
+size_t awq_gemm_epilogue_workspace_size(int64_t M, int64_t N, int64_t K, int bits,
+                                        int with_inv_s, unsigned flags) {
   if (M <= 0 || K <= 0 || N <= 0) return 0;
   (void)bits;
-  return fused_workspace(M, 1, N, K, false);
+  return fused_plan(M, 1, N, K, false, with_inv_s != 0, (flags & AWQ_GEMM_BF16) != 0).workspace;
 }
 
 awq_status awq_gemm_w4a16_epilogue(const awq_f16* X, int64_t M, const uint32_t* qweight,
@@ -1166,11 +1159,12 @@ awq_status awq_gemm_w4a16_epilogue(const awq_f16* X, int64_t M, const uint32_t* 
                     static_cast<cudaStream_t>(stream));
 }
 
-size_t awq_gemm_grouped_workspace_size(int64_t T, int64_t E, int64_t N, int64_t K, int bits) {
+size_t awq_gemm_grouped_workspace_size(int64_t T, int64_t E, int64_t N, int64_t K, int bits,
+                                       int with_inv_s, unsigned flags) {
   if (T <= 0 || E <= 0 || K <= 0 || N <= 0) return 0;
   (void)bits;
   if (E > awq::kMaxExperts) return 0;
-  return fused_workspace(T, E, N, K, true);
+  return fused_plan(T, E, N, K, true, with_inv_s != 0, (flags & AWQ_GEMM_BF16) != 0).workspace;
 }
 
 awq_status awq_gemm_w4a16_grouped(const awq_f16* X, int64_t T, const int32_t* offsets, int64_t E,

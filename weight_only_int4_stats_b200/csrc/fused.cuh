@@ -42,20 +42,10 @@ __device__ __forceinline__ float fused_bias(const FusedEpi& f, int64_t i) {
   return f.bias == nullptr ? 0.0f
                            : act_to_float<kBf16>(static_cast<const act_t<kBf16>*>(f.bias)[i]);
 }
-// Stores output i of Y from v = P + bias. mul and residual are read by the thread that writes
-// the output, before it does, so either may be Y itself.
-template <bool kBf16>
-__device__ __forceinline__ void fused_store(const FusedEpi& f, act_t<kBf16>* Y, int64_t i, float v) {
-  using A = act_t<kBf16>;
-  v = activate(v, f.act);
-  if (f.mul != nullptr) v *= act_to_float<kBf16>(static_cast<const A*>(f.mul)[i]);
-  if (f.residual != nullptr) v += act_to_float<kBf16>(static_cast<const A*>(f.residual)[i]);
-  Y[i] = float_to_act<kBf16>(v);
-}
-
-// The same for the four outputs a lane has of an m16n8 accumulator tile: rows n, n + 8 (value
-// i / 2) of tokens m, m + 1 (value i % 2). load() only loads: nothing waits for the values
-// until apply() uses them.
+// The epilogue of the four outputs a lane has of an m16n8 accumulator tile: weight rows n, n + 8
+// (value i / 2) of tokens m, m + 1 (value i % 2). load() only loads: nothing waits for the values
+// until apply() uses them. mul and residual are read by the thread that writes the output, before
+// it does, so either may be Y itself.
 template <bool kBf16>
 struct FusedIn {
   using A = act_t<kBf16>;
@@ -86,15 +76,16 @@ struct GroupTable {
   int tile[kMaxExperts + 1];   // token tiles before each expert, then their total
 };
 
-// Fills off[0 .. E] and tile[0 .. E] (one warp), for token tiles of bn rows. An offset outside
-// 0 .. M, or below one before it, is taken as the nearest value in order, so no row outside X
-// and Y is ever touched. offsets NULL: one expert with all M rows.
+// Fills off[0 .. E] and tile[0 .. E] for token tiles of bn rows: the whole CTA calls it, and
+// synchronises before it reads them. An offset outside 0 .. rows, or below one before it, is taken
+// as the nearest value in order, so no row outside X and Y is ever touched. offsets NULL: one
+// expert with all rows. (All offsets are loaded at once and then summed up from shared memory: a
+// warp that loads as it goes waits 600 cycles for every 32 experts.)
 __device__ __forceinline__ void build_group_table(int* off, int* tile, const int* offsets, int E,
                                                   int64_t rows, int bn) {
-  const int lane = threadIdx.x & 31;
   const int M = static_cast<int>(rows);
   if (offsets == nullptr) {
-    if (lane == 0) {
+    if (threadIdx.x == 0) {
       off[0] = 0;
       off[1] = M;
       tile[0] = 0;
@@ -102,30 +93,38 @@ __device__ __forceinline__ void build_group_table(int* off, int* tile, const int
     }
     return;
   }
+  for (int e = static_cast<int>(threadIdx.x); e <= E; e += static_cast<int>(blockDim.x)) {
+    const int v = offsets[e];
+    off[e] = v < 0 ? 0 : v > M ? M : v;
+  }
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  const int lane = threadIdx.x;
   int high = 0, tiles = 0;   // the last offset so far, the tiles before it
   for (int base = 0; base <= E; base += 32) {
     const int e = base + lane;
-    int v = e <= E ? offsets[e] : 0;
-    v = v < 0 ? 0 : v > M ? M : v;
-    if (lane == 0 && v < high) v = high;
+    int v = e <= E ? off[e] : M;
+    int before = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) before = high;
+    if (__any_sync(0xffffffffu, v < before)) {   // out of order: the running maximum
+      if (lane == 0 && v < high) v = high;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int w = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o && w > v) v = w;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int w = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o && w > v) v = w;
+      }
+      before = __shfl_up_sync(0xffffffffu, v, 1);
+      if (lane == 0) before = high;
+      if (e <= E) off[e] = v;
     }
-    const int before = __shfl_up_sync(0xffffffffu, v, 1);
     // the tiles of expert e - 1 end where expert e's begin
-    const int n = e == 0 || e > E ? 0 : v - (lane == 0 ? high : before);
-    int sum = (n + bn - 1) / bn;
+    int sum = e == 0 || e > E ? 0 : (v - before + bn - 1) / bn;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int w = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += w;
     }
-    if (e <= E) {
-      off[e] = v;
-      tile[e] = tiles + sum;
-    }
+    if (e <= E) tile[e] = tiles + sum;
     high = __shfl_sync(0xffffffffu, v, 31);
     tiles += __shfl_sync(0xffffffffu, sum, 31);
   }

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kGgThreads, 1)
   }
   pdl_wait();
   pdl_launch_dependents();
-  if (warp == 0) build_group_table(tab->off, tab->tile, args.offsets, args.E, args.M, BN);
+  build_group_table(tab->off, tab->tile, args.offsets, args.E, args.M, BN);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

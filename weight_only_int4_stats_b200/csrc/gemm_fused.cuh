@@ -233,22 +233,14 @@ __device__ __forceinline__ void dequant32(const uint32_t* w, uint32_t z, uint32_
       for (int q = 0; q < 4; ++q) o[4 * j + q] = v[q];
     }
   } else {
-    o[0] = raw3_qz<0, 0>(w[0], w[1], w[2], bias);
-    o[1] = raw3_qz<0, 1>(w[0], w[1], w[2], bias);
-    o[2] = raw3_qz<0, 2>(w[0], w[1], w[2], bias);
-    o[3] = raw3_qz<0, 3>(w[0], w[1], w[2], bias);
-    o[4] = raw3_qz<1, 0>(w[0], w[1], w[2], bias);
-    o[5] = raw3_qz<1, 1>(w[0], w[1], w[2], bias);
-    o[6] = raw3_qz<1, 2>(w[0], w[1], w[2], bias);
-    o[7] = raw3_qz<1, 3>(w[0], w[1], w[2], bias);
-    o[8] = raw3_qz<2, 0>(w[0], w[1], w[2], bias);
-    o[9] = raw3_qz<2, 1>(w[0], w[1], w[2], bias);
-    o[10] = raw3_qz<2, 2>(w[0], w[1], w[2], bias);
-    o[11] = raw3_qz<2, 3>(w[0], w[1], w[2], bias);
-    o[12] = raw3_qz<3, 0>(w[0], w[1], w[2], bias);
-    o[13] = raw3_qz<3, 1>(w[0], w[1], w[2], bias);
-    o[14] = raw3_qz<3, 2>(w[0], w[1], w[2], bias);
-    o[15] = raw3_qz<3, 3>(w[0], w[1], w[2], bias);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t v[4];
+      raw3_chunk<false>(w[0], w[1], w[2], j, v);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        o[4 * j + q] = h2_as_u32(__hsub2(u32_as_h2(v[q]), u32_as_h2(bias)));
+    }
   }
   if constexpr (!kInv) {
 #pragma unroll
@@ -408,7 +400,7 @@ __global__ void __launch_bounds__(kTfThreads, 1)
   // With `early` (one weight, not written by the preceding kernel) only what that kernel may
   // have written waits for it: X, mul, residual, Y, partial sums.
   if (!early) pdl_wait();
-  if (warp == 0) build_group_table(tab->off, tab->tile, args.offsets, args.E, args.M, BN);
+  build_group_table(tab->off, tab->tile, args.offsets, args.E, args.M, BN);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

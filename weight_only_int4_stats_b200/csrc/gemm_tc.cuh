@@ -237,10 +237,9 @@ __device__ __forceinline__ uint4 dequant_word_scaled_bf16(uint32_t w, uint32_t b
 // 32-k block whose low-bit words are w0 (offsets 0..15) / w1 (16..31) and whose bit-2 word
 // is w2 (the pair's two bits sit at bits hb and hb + 16; both are moved to bit 2 of their
 // 16-bit half by a single shift whose direction is fixed at compile time).
-// raw3_qz is the exact pair (q - z); dequant3_pair its product with the scale pair.
 template <int kI, int kE, bool kBf16 = false>
-__device__ __forceinline__ uint32_t raw3_qz(uint32_t w0, uint32_t w1, uint32_t w2,
-                                            uint32_t bias_lo) {
+__device__ __forceinline__ uint32_t dequant3_pair(uint32_t w0, uint32_t w1, uint32_t w2,
+                                                  uint32_t bias_lo, uint32_t sc2u) {
   constexpr int pp = 4 * (kI & 1) + kE;     // 2-bit field of the pair inside its low word
   constexpr int hb = 4 * kI + kE;           // bit of the pair inside the bit-2 word
   const uint32_t wlo = (kI < 2) ? w0 : w1;
@@ -250,15 +249,10 @@ __device__ __forceinline__ uint32_t raw3_qz(uint32_t w0, uint32_t w1, uint32_t w
   uint32_t v;
   // (hs & 0x00040004) | lo
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(hs), "r"(0x00040004u), "r"(lo));
-  if constexpr (kBf16) return b2_as_u32(__hsub2(u32_as_b2(v), u32_as_b2(bias_lo)));
-  else return h2_as_u32(__hsub2(u32_as_h2(v), u32_as_h2(bias_lo)));
-}
-template <int kI, int kE, bool kBf16 = false>
-__device__ __forceinline__ uint32_t dequant3_pair(uint32_t w0, uint32_t w1, uint32_t w2,
-                                                  uint32_t bias_lo, uint32_t sc2u) {
-  const uint32_t qz = raw3_qz<kI, kE, kBf16>(w0, w1, w2, bias_lo);
-  if constexpr (kBf16) return b2_as_u32(__hmul2(u32_as_b2(qz), u32_as_b2(sc2u)));
-  else return h2_as_u32(__hmul2(u32_as_h2(qz), u32_as_h2(sc2u)));
+  if constexpr (kBf16)
+    return b2_as_u32(__hmul2(__hsub2(u32_as_b2(v), u32_as_b2(bias_lo)), u32_as_b2(sc2u)));
+  else
+    return h2_as_u32(__hmul2(__hsub2(u32_as_h2(v), u32_as_h2(bias_lo)), u32_as_h2(sc2u)));
 }
 
 // Byte offset of 16-byte chunk c (k = 8c..8c+7) of row r in a 64-wide fp16 tile stored in

@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kG4Threads, 2) stream_fused_kernel(
   // The kernel before this one is prepare_rows_kernel, which lets this one start only after its
   // own predecessors have completed: offsets, weights and scales are there, and only what it
   // writes has to be waited for.
-  if (warp == 0) build_group_table(off, tile, a.offsets, a.E, a.T, tokens);
+  build_group_table(off, tile, a.offsets, a.E, a.T, tokens);
   __syncthreads();
   const int64_t total = static_cast<int64_t>(tile[a.E]) * ntiles;
   const int64_t P = gridDim.x, bx = blockIdx.x;

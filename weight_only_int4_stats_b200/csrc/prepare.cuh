@@ -15,6 +15,7 @@ namespace awq {
 //  * else plain rows [T, K], for the tensor-core kernel (gemm_fused.cuh).
 // The factors [T] follow the rows.
 constexpr int kPrepThreads = 256;
+constexpr int kPrepKeep = 4;   // 8-value chunks of a thread kept between the two passes
 
 template <bool kBf16>
 __device__ __forceinline__ void prep_load(float (&f)[8], const uint4* X, const float* inv_s, int64_t i) {
@@ -59,14 +60,29 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_rows_kernel(
   X += static_cast<int64_t>(row) * nch;
   float big = 0.0f;
   bool finite = true;
-  for (int i = tid; i < nch; i += kPrepThreads) {
-    float f[8];
-    prep_load<kBf16>(f, X, inv_s, i);
+  const auto look = [&](const float (&f)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       big = fmaxf(big, fabsf(f[e]));
       finite = finite && fabsf(f[e]) <= 3.4028235e38f;
     }
+  };
+  float keep[kPrepKeep][8];   // the row's first 8192 values stay in registers
+#pragma unroll
+  for (int j = 0; j < kPrepKeep; ++j) {
+    const int i = tid + j * kPrepThreads;
+    if (i < nch) {
+      prep_load<kBf16>(keep[j], X, inv_s, i);
+      look(keep[j]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) keep[j][e] = 0.0f;
+    }
+  }
+  for (int i = tid + kPrepKeep * kPrepThreads; i < nch; i += kPrepThreads) {
+    float f[8];
+    prep_load<kBf16>(f, X, inv_s, i);
+    look(f);
   }
   __shared__ float part[kPrepThreads / 32];
 #pragma unroll
@@ -81,11 +97,8 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_rows_kernel(
   const float up = __uint_as_float(static_cast<uint32_t>(127 + p) << 23);
   const int64_t row_bytes = static_cast<int64_t>(chunks) * chunk_bytes;
   uint8_t* base = out + (static_cast<int64_t>(row) << split) * row_bytes;
-  // whole groups (16 lanes each) per iteration: lanes past the row's end take part in the sums
-  for (int i = tid; i < (nch + 31) / 32 * 32; i += kPrepThreads) {
-    float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  const auto store = [&](int i, float (&f)[8]) {   // a whole warp: groups are 16 lanes each
     const bool live = i < nch;
-    if (live) prep_load<kBf16>(f, X, inv_s, i);
     const int g = i >> 4, ch = i & 15;   // 8-k chunk ch of the group: quarter ch / 4, j = ch % 4
     const int gl = g % chunk_groups;
     uint8_t* c = base + static_cast<int64_t>(g / chunk_groups) * chunk_bytes;
@@ -118,6 +131,15 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_rows_kernel(
           *reinterpret_cast<float*>(cp + chunk_groups * 256 + gl * 4) = sum * 5.9604644775390625e-8f;
       }
     }
+  };
+  const int padded = (nch + 31) / 32 * 32;
+#pragma unroll
+  for (int j = 0; j < kPrepKeep; ++j)
+    if (tid + j * kPrepThreads < padded) store(tid + j * kPrepThreads, keep[j]);
+  for (int i = tid + kPrepKeep * kPrepThreads; i < padded; i += kPrepThreads) {
+    float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (i < nch) prep_load<kBf16>(f, X, inv_s, i);
+    store(i, f);
   }
   if (tid == 0) {
     const int64_t rows_bytes =
