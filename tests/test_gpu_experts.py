@@ -315,11 +315,17 @@ def silu_mul_tolerance(X, Wg, Wu):
     return h, tol + 8 * 2.0 ** -24 * np.abs(G * U_) + 2.0 ** -11 * (np.abs(h) + tol) + 2.0 ** -25
 
 
-@pytest.mark.parametrize("group", range(len(GROUPS)))
-@pytest.mark.parametrize("I,K", [(144, 256), (37, 384), (300, 1024)])
-def test_silu_mul_grouped_against_64_bits(awq, group, I, K):
-    counts, before, behind = GROUPS[group]
-    rng = np.random.default_rng([group, I, K])
+# small layers (tiles of 64 rows of each weight), then layers whose tiles of 128 rows fill the GPU
+# once, for each token tile
+SILU = [(c, b, e, I, K) for c, b, e in GROUPS for I, K in ((144, 256), (37, 384), (300, 1024))] + [
+    ([64, 1, 0, 33, 200], 2, 1, 3000, 256), ([400, 300], 0, 0, 5000, 128),
+    ([10, 0, 7, 30], 0, 3, 4500, 128)]
+
+
+@pytest.mark.parametrize("case", range(len(SILU)))
+def test_silu_mul_grouped_against_64_bits(awq, case):
+    counts, before, behind, I, K = SILU[case]
+    rng = np.random.default_rng([case, I, K])
     E = len(counts)
     off = offsets_of(counts, before)
     T = int(off[-1]) + behind

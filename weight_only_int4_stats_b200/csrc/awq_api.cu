@@ -1104,14 +1104,14 @@ awq_status fused_gemm(const void* X, int64_t T, const int32_t* offsets, int64_t 
               : launch_pdl(awq::splitk_fused_kernel<false>, grid, 256, 0, st, args);
 }
 
-template <int BN>
-awq_status launch_gated(const void* X, const void* gate, const void* up, awq::FusedArgs a,
+template <int BN, bool kStack>
+awq_status launch_gated_tiles(const void* X, const void* gate, const void* up, awq::FusedArgs a,
                         cudaStream_t st) {
-  using L = awq::GgLayout<BN>;
+  using L = awq::GgLayout<BN, kStack>;
   static std::atomic<bool> attr_set[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return AWQ_ERR_CUDA;
-  auto kern = awq::gated_grouped_kernel<BN>;
+  auto kern = awq::gated_grouped_kernel<BN, kStack>;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem) !=
         cudaSuccess)
@@ -1120,17 +1120,33 @@ awq_status launch_gated(const void* X, const void* gate, const void* up, awq::Fu
   }
   CUtensorMap tx, tg, tu;
   if (!make_tmap_2d(&tx, X, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.M, a.K, BN, awq::kTcBK, true) ||
-      !make_tmap_2d(&tg, gate, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.E * a.N, a.K, awq::kTcBM,
+      !make_tmap_2d(&tg, gate, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.E * a.N, a.K, L::kRows,
                     awq::kTcBK, true) ||
-      !make_tmap_2d(&tu, up, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.E * a.N, a.K, awq::kTcBM,
+      !make_tmap_2d(&tu, up, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.E * a.N, a.K, L::kRows,
                     awq::kTcBK, true))
     return AWQ_ERR_CUDA;
-  a.row_tiles = static_cast<int>((a.N + awq::kTcBM - 1) / awq::kTcBM);
+  a.row_tiles = static_cast<int>((a.N + L::kRows - 1) / L::kRows);
   const int64_t units = a.row_tiles * (a.M / BN + (a.M < a.E ? a.M : a.E));
   if (units > kMaxDim) return AWQ_ERR_INVALID_ARG;   // the kernel counts them in 32 bits
   const int64_t sms = num_sms();
   return launch_pdl(kern, dim3(static_cast<unsigned>(units < sms ? units : sms)), awq::kGgThreads,
                     L::kSmem, st, tx, tg, tu, a);
+}
+
+// Tiles of 128 rows of both weights, or of 64 where those take fewer rounds of the CTAs (1003 rows
+// over 16 experts of [1536, 2048], some 204 tiles of 128: 45 us, and 42 of 64). How many token
+// tiles the experts make is known on the device only: one each and some more where the mean row
+// count is well below BN, the full ones and half a tile each where it is not.
+template <int BN>
+awq_status launch_gated(const void* X, const void* gate, const void* up, const awq::FusedArgs& a,
+                        cudaStream_t st) {
+  const int64_t sms = num_sms();
+  const int64_t active = a.M < a.E ? a.M : a.E;
+  const int64_t tokens = 3 * a.M <= 2 * BN * a.E ? active + active / 12 : a.M / BN + active / 2;
+  const int64_t whole = ((a.N + 127) / 128 * tokens + sms - 1) / sms;
+  const int64_t half = ((a.N + 63) / 64 * tokens + sms - 1) / sms;
+  return 10 * half < 19 * whole ? launch_gated_tiles<BN, true>(X, gate, up, a, st)
+                                : launch_gated_tiles<BN, false>(X, gate, up, a, st);
 }
 
 bool bad_groups(int64_t E, const int32_t* offsets) {

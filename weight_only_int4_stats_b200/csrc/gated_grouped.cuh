@@ -4,12 +4,19 @@
 // Tensor-bound. One tile is 128 rows of both weights (two A tiles and two TMEM accumulators)
 // against up to BN tokens of one expert; units (expert, row tile, token tile) go round the
 // persistent CTAs in gemm_fused.cuh's order, and the whole MMA warp walks the issue loop.
+// Measured: 16384 rows over 8 experts of [14336, 4096] 3.6 ms, 1050 TFLOP/s at the power limit's
+// 1.45 GHz; 1003 rows over 16 experts of [1536, 2048] 42 us, where 189 MB of weights would take
+// 29 us (45 us in tiles of 128 rows, some 204 of which make two rounds of the 148 SMs).
 //   warp 0       TMA producer of X and both weights, in stages of 64 k
 //   warp 1       TMEM allocator and MMA issuer
 //   warps 2, 3   idle
 //   warps 4..11  epilogue: two warps per TMEM lane quarter, each half of the token columns (with
 //                BN = 256 the accumulators fill TMEM, so the next tile waits for this one's
 //                epilogue: eight warps and the fast exponential and division keep that short)
+// kStack: 64 rows of each weight in one A tile of 128 (gate above up) and one accumulator, for calls
+// of few tiles: half as much work a tile fills the last round of CTAs better, at twice the reads
+// of X. The up half of the accumulator lies in other warps' TMEM lanes than the gate half, so it
+// goes through shared memory.
 #pragma once
 #include "common.cuh"
 #include "fused.cuh"
@@ -20,26 +27,30 @@ namespace awq {
 constexpr int kGgThreads = 12 * 32;
 constexpr int kGgEpiWarp0 = 4;
 
-template <int BN>
+template <int BN, bool kStack>
 struct GgLayout {
+  static constexpr int kRows = kStack ? 64 : 128;            // of each weight in a tile
   static constexpr int kXBytes = BN * kTcBK * 2;
-  static constexpr int kABytes = kTcBM * kTcBK * 2;          // of one weight
+  static constexpr int kABytes = kRows * kTcBK * 2;          // of one weight
   static constexpr int kStage = kXBytes + 2 * kABytes;
-  static constexpr int kStages = BN == 256 ? 3 : BN == 128 ? 4 : 5;
-  static constexpr int kBufs = 4 * BN <= 512 ? 2 : 1;        // accumulator pairs in TMEM
-  static constexpr uint32_t kCols = 2 * BN * kBufs;
-  static constexpr int kBarOff = kStages * kStage;
+  static constexpr int kStages = kStack ? (BN == 256 ? 4 : BN == 128 ? 6 : 8)
+                                        : (BN == 256 ? 3 : BN == 128 ? 4 : 5);
+  static constexpr int kAccCols = kStack ? BN : 2 * BN;      // of a tile's accumulators
+  static constexpr int kBufs = 2 * kAccCols <= 512 ? 2 : 1;
+  static constexpr uint32_t kCols = kAccCols * kBufs;
+  static constexpr int kXchgOff = kStages * kStage;          // kStack: up values on their way
+  static constexpr int kBarOff = kXchgOff + (kStack ? 2 * 4 * 16 * 32 * 4 : 0);
   static constexpr int kTabOff = kBarOff + 256;
   static constexpr int kSmem = kTabOff + static_cast<int>(sizeof(GroupTable)) + 1024;
   static_assert(kSmem <= kTcSmemMax && (2 * kStages + 4) * 8 + 8 <= 256, "shared memory");
 };
 
-template <int BN>
+template <int BN, bool kStack>
 __global__ void __launch_bounds__(kGgThreads, 1)
     gated_grouped_kernel(const __grid_constant__ CUtensorMap tmap_x,
                          const __grid_constant__ CUtensorMap tmap_g,
                          const __grid_constant__ CUtensorMap tmap_u, const FusedArgs args) {
-  using L = GgLayout<BN>;
+  using L = GgLayout<BN, kStack>;
   constexpr int S = L::kStages, B = L::kBufs;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -90,7 +101,7 @@ __global__ void __launch_bounds__(kGgThreads, 1)
       bool ok = true;
       for (unsigned u = blockIdx.x; u < units && ok; u += gridDim.x) {
         const TfUnit t = tf_unit<BN>(u, args, tab, G);
-        const int arow = static_cast<int>(t.e * args.N) + t.row0;
+        const int arow = static_cast<int>(t.e * args.N) + (kStack ? t.row0 / 2 : t.row0);
         for (int i = 0; i < 2 * G; ++i) {
           ok = mbar_wait(&empty[s], ph ^ 1);
           if (!ok) break;
@@ -111,7 +122,7 @@ __global__ void __launch_bounds__(kGgThreads, 1)
     for (unsigned u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const TfUnit t = tf_unit<BN>(u, args, tab, G);
       const uint32_t idesc = f16_idesc(kTcBM, (t.cols + 15) / 16 * 16);
-      const uint32_t d = tmem + buf * 2 * BN;
+      const uint32_t d = tmem + buf * L::kAccCols;
       ok = __all_sync(0xffffffffu, mbar_wait(&dempty[buf], dph ^ 1));
       for (int i = 0; i < 2 * G && ok; ++i) {
         ok = __all_sync(0xffffffffu, mbar_wait(&full[s], ph));
@@ -125,7 +136,7 @@ __global__ void __launch_bounds__(kGgThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             tc_mma_f16(d, gd + 2 * k, xd + 2 * k, idesc, (i | k) != 0 ? 1u : 0u);
-            tc_mma_f16(d + BN, ud + 2 * k, xd + 2 * k, idesc, (i | k) != 0 ? 1u : 0u);
+            if (!kStack) tc_mma_f16(d + BN, ud + 2 * k, xd + 2 * k, idesc, (i | k) != 0 ? 1u : 0u);
           }
           tc_commit(&empty[s]);
           if (i == 2 * G - 1) tc_commit(&dfull[buf]);
@@ -138,24 +149,47 @@ __global__ void __launch_bounds__(kGgThreads, 1)
   } else if (warp >= kGgEpiWarp0) {
     // ------------------------------------------------------------------ epilogue
     const int half = (warp - kGgEpiWarp0) >> 2;
-    const int row = 32 * (warp & 3) + lane;
-    const uint32_t td = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const int quarter = warp & 3;
+    // kStack: quarters 0 and 1 hold gate, 2 and 3 the same rows' up
+    const int row = 32 * (kStack ? quarter & 1 : quarter) + lane;
+    const uint32_t td = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+    float* xchg = reinterpret_cast<float*>(smem + L::kXchgOff) + (2 * half + (quarter & 1)) * 512 + lane;
     __half* H = static_cast<__half*>(args.Y);
-    int buf = 0;
+    int buf = 0, parity = 0;
     uint32_t ph = 0;
+    // after a wait that ran out the warps still walk their tiles, without waiting or storing, so
+    // that a pair of kStack does not part at its named barrier
+    bool ok = true;
     for (unsigned u = blockIdx.x; u < units; u += gridDim.x) {
       const TfUnit t = tf_unit<BN>(u, args, tab, G);
-      const int64_t n = t.row0 + row;
+      const int64_t n = (kStack ? t.row0 / 2 : t.row0) + row;
       const bool live = n < args.N && AWQ_IN_BOUNDS(t.m0 + t.cols <= args.M && t.e < args.E);
-      if (!__all_sync(0xffffffffu, mbar_wait(&dfull[buf], ph))) break;
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&dfull[buf], ph));
       tc_fence_after();
 #pragma unroll 1
       for (int c0 = 16 * half; c0 < t.cols; c0 += 32) {
         uint32_t g[16], v[16];
-        tmem_ld_32x32b_x16(td + buf * 2 * BN + c0, g);
-        tmem_ld_32x32b_x16(td + buf * 2 * BN + BN + c0, v);
-        tmem_ld_wait();
-        if (live) {
+        tmem_ld_32x32b_x16(td + buf * L::kAccCols + c0, g);
+        if constexpr (kStack) {
+          // up's warp hands its values to gate's; the buffer alternates, so one barrier a turn
+          // also tells that the values before the last have been read
+          tmem_ld_wait();
+          float* x = xchg + parity * 2048;
+          parity ^= 1;
+          if (quarter >= 2) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j * 32] = __uint_as_float(g[j]);
+          }
+          named_bar_sync(1 + 2 * half + (quarter & 1), 64);
+          if (quarter < 2) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(x[j * 32]);
+          }
+        } else {
+          tmem_ld_32x32b_x16(td + buf * L::kAccCols + BN + c0, v);
+          tmem_ld_wait();
+        }
+        if (ok && live && (!kStack || quarter < 2)) {
           __half* h = H + static_cast<int64_t>(t.m0 + c0) * args.N + n;
 #pragma unroll
           for (int j = 0; j < 16; ++j)
@@ -167,7 +201,7 @@ __global__ void __launch_bounds__(kGgThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&dempty[buf]);
+      if (ok && lane == 0) mbar_arrive(&dempty[buf]);
       if (++buf == B) { buf = 0; ph ^= 1; }
     }
   }

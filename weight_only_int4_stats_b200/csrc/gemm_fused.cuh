@@ -31,6 +31,12 @@
 // of two per row (with inv_s already in), and the epilogue takes the row's factor off. bf16
 // weights would need (q - z) * scale in two bf16 parts to be rounded only once (19 operations a
 // word of 8 codes, 45 with inv_s, against 13), and the dequantization is what bounds this kernel.
+// Measured: 8 experts of [14336, 4096] with 128 rows 93 us, 2.6 TB/s of packed weights; with 2048
+// rows 279 us, 863 TFLOP/s; [14336, 4096] x 4096 tokens 425 us, 1130 TFLOP/s. Few rows: the
+// dequantization (13 operations a word of 8 codes; 24 at 3 bits) on 4 warps a scheduler, and
+// their barriers. Many rows, run for long: the 1000 W power limit, under which the SM clock falls to
+// 1.45 GHz (2.1 ms for 8 experts of [4096, 14336] with 16384 rows), and about 200 cycles a group
+// that the MMA issuer spends waiting and counting.
 // Packed codes: 4 bits: boxes of 128 rows x 128 bytes (two groups) with the 128-byte swizzle;
 // 3 bits: one box of 3 or 5 groups (an odd multiple of 48 bytes per row, so that the 16-byte
 // reads of eight consecutive rows fall into eight different bank groups as they are).
