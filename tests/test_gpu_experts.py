@@ -319,7 +319,7 @@ def silu_mul_tolerance(X, Wg, Wu):
 # once, for each token tile
 SILU = [(c, b, e, I, K) for c, b, e in GROUPS for I, K in ((144, 256), (37, 384), (300, 1024))] + [
     ([64, 1, 0, 33, 200], 2, 1, 3000, 256), ([400, 300], 0, 0, 5000, 128),
-    ([10, 0, 7, 30], 0, 3, 4500, 128)]
+    ([10, 0, 7, 30], 0, 3, 4500, 128), ([150, 100, 140], 1, 0, 5000, 128)]
 
 
 @pytest.mark.parametrize("case", range(len(SILU)))

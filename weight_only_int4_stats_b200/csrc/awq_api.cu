@@ -1133,19 +1133,20 @@ awq_status launch_gated_tiles(const void* X, const void* gate, const void* up, a
                     L::kSmem, st, tx, tg, tu, a);
 }
 
-// Tiles of 128 rows of both weights, or of 64 where those take fewer rounds of the CTAs (1003 rows
-// over 16 experts of [1536, 2048], some 204 tiles of 128: 45 us, and 42 of 64). How many token
-// tiles the experts make is known on the device only: one each and some more where the mean row
-// count is well below BN, the full ones and half a tile each where it is not.
+// Tiles for experts of few rows: 128 rows of both weights, or 64 where those take clearly fewer
+// rounds of the CTAs, counted with one token tile an expert and some more (us in tiles of 128 and
+// of 64: 1003 rows over 16 experts of [1536, 2048] 46 and 41, 2400 rows 90 and 72, 300 over 4 of
+// [2048, 4096] 35 and 30; but 1200 over 8 of [4096, 4096] 112 and 126, 8192 over 64 of
+// [1408, 2048] 154 and 174, where the rounds only double and X is read twice as often).
 template <int BN>
 awq_status launch_gated(const void* X, const void* gate, const void* up, const awq::FusedArgs& a,
                         cudaStream_t st) {
   const int64_t sms = num_sms();
   const int64_t active = a.M < a.E ? a.M : a.E;
-  const int64_t tokens = 3 * a.M <= 2 * BN * a.E ? active + active / 12 : a.M / BN + active / 2;
+  const int64_t tokens = active + active / 12;
   const int64_t whole = ((a.N + 127) / 128 * tokens + sms - 1) / sms;
   const int64_t half = ((a.N + 63) / 64 * tokens + sms - 1) / sms;
-  return 10 * half < 19 * whole ? launch_gated_tiles<BN, true>(X, gate, up, a, st)
+  return 10 * half < 16 * whole ? launch_gated_tiles<BN, true>(X, gate, up, a, st)
                                 : launch_gated_tiles<BN, false>(X, gate, up, a, st);
 }
 
@@ -1219,7 +1220,17 @@ awq_status awq_silu_mul_gemm_grouped(const awq_f16* X, int64_t T, const int32_t*
   const int64_t rows = (T + E - 1) / E * 3 / 2;
   if (rows <= 64) return launch_gated<64>(X, W_gate, W_up, args, st);
   if (rows <= 128) return launch_gated<128>(X, W_gate, W_up, args, st);
-  return launch_gated<256>(X, W_gate, W_up, args, st);
+  if (rows <= 256) return launch_gated<256>(X, W_gate, W_up, args, st);
+  // Many rows: tiles of 64, whose one accumulator leaves room for a second one, so that epilogues
+  // overlap; but of 128, which read X once, where a call is long enough for the power limit and K
+  // for the epilogues not to count (us in tiles of 128 and of 64: 4096 rows over 8 experts of
+  // [14336, 4096] 995 and 981, 32768 over 64 of [1536, 2048] 433 and 420, 8192 over 8 of
+  // [14336, 1024] 583 and 492; 16384 over 8 of [14336, 4096] 3455 and 3552, 32768 over 8 of
+  // [4096, 4096] 1888 and 1964).
+  const int64_t tiles = (args.N + 127) / 128 * (T / 256 + (T < E ? T : E) / 2);
+  if (K >= 4096 && tiles > 16 * num_sms())
+    return launch_gated_tiles<256, false>(X, W_gate, W_up, args, st);
+  return launch_gated_tiles<256, true>(X, W_gate, W_up, args, st);
 }
 
 // ------------------------------------------------------------------ act_stats of each expert

@@ -4,19 +4,20 @@
 // Tensor-bound. One tile is 128 rows of both weights (two A tiles and two TMEM accumulators)
 // against up to BN tokens of one expert; units (expert, row tile, token tile) go round the
 // persistent CTAs in gemm_fused.cuh's order, and the whole MMA warp walks the issue loop.
-// Measured: 16384 rows over 8 experts of [14336, 4096] 3.6 ms, 1050 TFLOP/s at the power limit's
-// 1.45 GHz; 1003 rows over 16 experts of [1536, 2048] 42 us, where 189 MB of weights would take
-// 29 us (45 us in tiles of 128 rows, some 204 of which make two rounds of the 148 SMs).
+// Measured: 16384 rows over 8 experts of [14336, 4096] 3.45 to 3.65 ms, 1050 to 1115
+// TFLOP/s under the power limit; 1003 rows over 16 experts of [1536, 2048] 41 us, where 189 MB of
+// weights would take 29 us.
 //   warp 0       TMA producer of X and both weights, in stages of 64 k
 //   warp 1       TMEM allocator and MMA issuer
 //   warps 2, 3   idle
 //   warps 4..11  epilogue: two warps per TMEM lane quarter, each half of the token columns (with
 //                BN = 256 the accumulators fill TMEM, so the next tile waits for this one's
 //                epilogue: eight warps and the fast exponential and division keep that short)
-// kStack: 64 rows of each weight in one A tile of 128 (gate above up) and one accumulator, for calls
-// of few tiles: half as much work a tile fills the last round of CTAs better, at twice the reads
-// of X. The up half of the accumulator lies in other warps' TMEM lanes than the gate half, so it
-// goes through shared memory.
+// kStack: 64 rows of each weight in one A tile of 128 (gate above up) and one accumulator, so that
+// there is room for a second one and the epilogue overlaps the next tile even with BN = 256, and
+// half as much work a tile fills the last round of CTAs better; X is read twice as often. The up
+// half of the accumulator lies in other warps' TMEM lanes than the gate half, so the warps of a
+// pair trade tokens through shared memory.
 #pragma once
 #include "common.cuh"
 #include "fused.cuh"
@@ -171,29 +172,39 @@ __global__ void __launch_bounds__(kGgThreads, 1)
         uint32_t g[16], v[16];
         tmem_ld_32x32b_x16(td + buf * L::kAccCols + c0, g);
         if constexpr (kStack) {
-          // up's warp hands its values to gate's; the buffer alternates, so one barrier a turn
-          // also tells that the values before the last have been read
+          // up's warp hands over the first 8 tokens, gate's the last 8, and each finishes its 8;
+          // the buffer alternates, so one barrier a turn also tells that the values before the
+          // last have been read
           tmem_ld_wait();
           float* x = xchg + parity * 2048;
           parity ^= 1;
           if (quarter >= 2) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j * 32] = __uint_as_float(g[j]);
+            for (int j = 0; j < 8; ++j) x[j * 32] = __uint_as_float(g[j]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = g[8 + j];
+          } else {
+#pragma unroll
+            for (int j = 8; j < 16; ++j) x[j * 32] = __uint_as_float(g[j]);
           }
           named_bar_sync(1 + 2 * half + (quarter & 1), 64);
-          if (quarter < 2) {
+          if (quarter >= 2) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(x[j * 32]);
+            for (int j = 0; j < 8; ++j) g[j] = __float_as_uint(x[(8 + j) * 32]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(x[j * 32]);
           }
         } else {
           tmem_ld_32x32b_x16(td + buf * L::kAccCols + BN + c0, v);
           tmem_ld_wait();
         }
-        if (ok && live && (!kStack || quarter < 2)) {
-          __half* h = H + static_cast<int64_t>(t.m0 + c0) * args.N + n;
+        const int c1 = kStack && quarter >= 2 ? c0 + 8 : c0;
+        if (ok && live) {
+          __half* h = H + static_cast<int64_t>(t.m0 + c1) * args.N + n;
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c0 + j < t.cols)
+          for (int j = 0; j < (kStack ? 8 : 16); ++j)
+            if (c1 + j < t.cols)
               h[j * args.N] = __float2half_rn(activate(__uint_as_float(g[j]), kActSilu) *
                                               __uint_as_float(v[j]));
         }
