@@ -216,7 +216,8 @@ AWQ_API awq_status awq_silu_mul_gemm(const awq_f16* X, int64_t M, const awq_f16*
  * AWQ_GEMM_WEIGHTS_READY states that qweight, scales and zeros are NOT written by the kernel
  * launched immediately before this call on `stream` (they were written earlier, e.g. model
  * weights loaded once): the decode kernel then starts streaming them at once, overlapping
- * the preceding kernel. X is always read only after the preceding kernel has completed.
+ * the preceding kernel. X and inv_s are always read only after the preceding kernel has
+ * completed.
  * (This library's kernels let the next launch start only after their own predecessor has
  * completed, so with them the window is exactly one kernel.)
  * AWQ_GEMM_BF16: X and Y are bf16 instead of fp16 (sourcepulse.org "AWQ", "Maintenance &

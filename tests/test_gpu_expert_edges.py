@@ -1,0 +1,45 @@
+"""The products with a fused epilogue and the expert operators where their rules meet: inputs that
+the kernel just before writes, the ends of the value ranges, each path's own precision."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_experts import BF16, F16, Layer, awq, cu, dense, tokens  # noqa: F401 (awq: fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# M, N, K, bits, dtype: the streaming kernel, then the tensor-core kernel with and without slices of
+# K, at each size of its token tile
+@pytest.mark.parametrize("M,N,K,bits,dtype", [
+    (1, 512, 2048, 4, F16), (3, 512, 2048, 3, F16), (8, 512, 2048, 4, BF16), (6, 512, 2048, 4, F16),
+    (30, 512, 4096, 3, F16), (64, 4096, 1024, 4, F16), (77, 512, 11008, 4, F16),
+    (128, 512, 1024, 3, F16), (300, 1024, 1024, 4, F16), (40, 512, 1024, 4, BF16)])
+def test_inv_s_from_the_kernel_just_before(awq, M, N, K, bits, dtype):  # noqa: F811
+    """weights_ready speaks of the packed weights alone: factors that the preceding kernel is
+    still writing when this call's kernels start (the statistics let the next launch start before
+    they store) are read after it has stored them."""
+    rng = np.random.default_rng([M, N, K])
+    layer = Layer(rng, 1, N, K, bits, dtype)
+    X = tokens(rng, M, K, dtype)
+    rows = tokens(rng, 2048, K, F16)
+    sides, off = (rows, rows * 4), cu(np.array([0, 2048], np.int32))
+    inv = torch.empty(1, K, device="cuda")
+
+    def product():
+        return awq.awq_gemm_w4a16_epilogue(X, layer.qw[0], layer.sc[0], layer.z[0], N, K, bits,
+                                           inv_s=inv[0], weights_ready=True)
+
+    want = []
+    for side in sides:
+        awq.awq_act_stats_grouped(side, off, out=inv)
+        torch.cuda.synchronize()
+        want.append(product())
+        torch.cuda.synchronize()
+    assert torch.allclose(want[1].float(), 4 * want[0].float(), rtol=2.0 ** -6, atol=1e-2)
+    assert not torch.equal(want[0], want[1])
+    for turn in range(24):
+        awq.awq_act_stats_grouped(sides[turn % 2], off, out=inv)
+        y = product()
+        assert torch.equal(y, want[turn % 2]), turn
+    awq.awq_check_error()

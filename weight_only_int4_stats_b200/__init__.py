@@ -370,7 +370,8 @@ def awq_gemm_w4a16_epilogue(X: torch.Tensor, qweight: torch.Tensor, scales: torc
 
     X fp16 or bf16 [M, K]; bias [N], mul and residual [M, N] in X's dtype, each optional; act a
     key of ACTIVATIONS. ``out`` may be ``mul`` or ``residual`` itself. ``weights_ready`` as for
-    awq_gemm_w4a16."""
+    awq_gemm_w4a16: it speaks of qweight, scales and zeros alone, everything else may come from
+    the kernel launched just before."""
     dev, t, M = X.get_device(), X.dtype, X.shape[0]
     x, G = _activations(X, K, dev), K // GROUP
     flags = (WEIGHTS_READY if weights_ready else 0) | (BF16 if t is torch.bfloat16 else 0)

@@ -13,8 +13,8 @@
 // block's columns of its lane.
 //   warp 0       TMA producer of X
 //   warp 1       TMEM allocator and single-thread tcgen05.mma issuer
-//   warp 2       TMA producer of packed codes (and inv_s), prefetch of scales and zero points
-//   warp 3       idle
+//   warp 2       TMA producer of packed codes, prefetch of scales and zero points
+//   warp 3       producer of inv_s, into the packed codes' slots (idle without it)
 //   warps 4..19  builders: four sets of four warps (a warp reaches the TMEM lanes of its quarter,
 //                warp % 4); the sets take the K blocks in turn, so that four chains of
 //                shared-memory reads, arithmetic, TMEM stores and barriers run at once
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kTfThreads, 1)
       mbar_init(&aempty[i], 1);
     }
     for (int i = 0; i < P; ++i) {
-      mbar_init(&pfull[i], 1);
+      mbar_init(&pfull[i], kInv ? 2 : 1);   // the codes' producer, and that of inv_s
       mbar_init(&pempty[i], 4 * kTfSets);   // every builder warp
     }
     for (int i = 0; i < 2; ++i) {
@@ -403,8 +403,9 @@ __global__ void __launch_bounds__(kTfThreads, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  // With `early` (one weight, not written by the preceding kernel) only what that kernel may
-  // have written waits for it: X, mul, residual, Y, partial sums.
+  // With `early` (one weight, whose codes, scales and zero points the preceding kernel does not
+  // write) only what that kernel may have written waits for it, each in the warps that touch it: X,
+  // inv_s, bias, mul, residual, Y, partial sums.
   if (!early) pdl_wait();
   build_group_table(tab->off, tab->tile, args.offsets, args.E, args.M, BN);
   tc_fence_before();
@@ -496,17 +497,11 @@ __global__ void __launch_bounds__(kTfThreads, 1)
         if (lane == 0) {
           // groups past K are zero codes that nothing uses; a box is always counted whole
           const int32_t arow = static_cast<int32_t>(t.e * args.N) + t.row0;
-          const uint32_t inv_bytes =
-              kInv ? static_cast<uint32_t>((G - g < kPG ? G - g : kPG) * kGroup * 4) : 0u;
-          mbar_arrive_expect_tx(&pfull[ps], L::kBoxes * L::kBoxBytes + inv_bytes);
+          mbar_arrive_expect_tx(&pfull[ps], L::kBoxes * L::kBoxBytes);
 #pragma unroll
           for (int b = 0; b < L::kBoxes; ++b)
             tma_load_2d(smem + L::kPOff + ps * L::kPBytes + b * L::kBoxBytes, &tmap_w, &pfull[ps],
                         kBits == 4 ? (g + 2 * b) * 16 : g * 12, arow);
-          if (inv_bytes != 0 && AWQ_IN_BOUNDS(g < G))
-            bulk_load_1d(smem + L::kIOff + ps * L::kInvBytes,
-                         args.inv_s + (static_cast<int64_t>(t.e) * G + g) * kGroup, inv_bytes,
-                         &pfull[ps]);
         }
         // scales (256 bytes a group) and zero points (128) of the slot towards L2
         const int pg = g + lane / 4;
@@ -519,6 +514,30 @@ __global__ void __launch_bounds__(kTfThreads, 1)
                              : static_cast<const void*>(args.zeros + x)));
         }
         if (++ps == P) { ps = 0; ph ^= 1; }
+      }
+    }
+  } else if (kInv && warp == 3) {
+    // ------------------------------------------------------------------ inv_s producer
+    // The factors are no part of the packed weight: the preceding kernel may have written them, so
+    // they wait for it where the codes need not.
+    pdl_wait();
+    if (lane == 0) {
+      int ps = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (unsigned u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        const TfUnit t = tf_unit<BN>(u, args, tab, G);
+        for (int i = 0; i < t.groups; i += kPG) {   // the slots of the packed producer
+          ok = mbar_wait(&pempty[ps], ph ^ 1);
+          if (!ok) break;
+          const int g = t.g0 + i;
+          const uint32_t bytes = static_cast<uint32_t>((G - g < kPG ? G - g : kPG) * kGroup * 4);
+          mbar_arrive_expect_tx(&pfull[ps], bytes);
+          if (AWQ_IN_BOUNDS(g < G && t.e < args.E))
+            bulk_load_1d(smem + L::kIOff + ps * L::kInvBytes,
+                         args.inv_s + (static_cast<int64_t>(t.e) * G + g) * kGroup, bytes, &pfull[ps]);
+          if (++ps == P) { ps = 0; ph ^= 1; }
+        }
       }
     }
   } else if (warp >= kTfBuildWarp0 && warp < kTfEpiWarp0) {
