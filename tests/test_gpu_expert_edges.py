@@ -43,3 +43,38 @@ def test_inv_s_from_the_kernel_just_before(awq, M, N, K, bits, dtype):  # noqa: 
         y = product()
         assert torch.equal(y, want[turn % 2]), turn
     awq.awq_check_error()
+
+
+# the streaming kernel (one and two rows a token), the tensor-core kernel with and without slices of K
+@pytest.mark.parametrize("M,N,K,bits,inv", [(3, 144, 1024, 4, True), (8, 37, 384, 3, True),
+                                            (5, 4400, 7808, 4, False), (40, 130, 512, 4, True),
+                                            (77, 512, 4096, 4, False), (300, 257, 256, 3, True)])
+@pytest.mark.parametrize("e", [118, 70, -70, -112])
+def test_bf16_rows_at_the_ends_of_the_range(awq, M, N, K, bits, inv, e):  # noqa: F811
+    """Rows times 2^e give outputs times 2^e: every step is a product or a sum, and none leaves the
+    range of fp32 on the way (|P| < 2^9 here). Outputs that become subnormal are off by a step."""
+    rng = np.random.default_rng([M, N, K])
+    layer = Layer(rng, 1, N, K, bits, BF16, inv)
+    X = tokens(rng, M, K, BF16).clamp(-8, 8)
+    base = dense(awq, layer, X).float()
+    assert base.abs().max() < 512
+    y = dense(awq, layer, X * 2.0 ** e).float()
+    awq.awq_check_error()
+    back = y.double() * 2.0 ** -e   # (a Python power: exact)
+    step = 2.0 ** (-133 - e)   # of bf16's subnormals, seen from the base's scale
+    assert ((back - base.double()).abs() <= (step if e < -100 else 0)).all()
+
+
+def test_a_row_of_each_size_beside_the_others(awq):  # noqa: F811
+    """Each row has its own power of two: a tiny and a huge row do not notice one another."""
+    rng = np.random.default_rng(1)
+    layer = Layer(rng, 1, 96, 256, 4, BF16)
+    for M in (7, 50):
+        X = tokens(rng, M, 256, BF16).clamp(-8, 8)
+        X[-1] = 0
+        e = np.linspace(-100, 118, M).round().astype(int)   # (powers of two by ldexp: exact)
+        up, down = (torch.from_numpy(np.ldexp(1.0, k)[:, None]).cuda() for k in (e, -e))
+        y = dense(awq, layer, (X.double() * up).to(BF16))
+        want = dense(awq, layer, X)
+        assert torch.equal(y.double() * down, want.double())
+        assert (y[-1] == 0).all()

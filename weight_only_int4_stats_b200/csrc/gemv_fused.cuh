@@ -472,13 +472,15 @@ __global__ void __launch_bounds__(kG4Threads, 2) stream_fused_kernel(
           v[0] += v[1];
           v[2] += v[3];
         }
+        // (the codes came in as q 2^-24; the products by 2^24 and the factor, one after the other,
+        // leave fp32's range only where the result does)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int m = fm + (i & 1);
           const int64_t n = fn + 8 * (i >> 1);
           if (m < cur.rows && n < a.N && !(a.split && (i & 1)) && AWQ_IN_BOUNDS(cur.m0 + m < a.T))
             static_cast<A*>(a.Y)[(static_cast<int64_t>(cur.m0) + m) * a.N + n] =
-                float_to_act<kBf16>(fin.apply(epi, v[i] * fs[i & 1], i));
+                float_to_act<kBf16>(fin.apply(epi, v[i] * 16777216.0f * fs[i & 1], i));
         }
       }
       chunk = 0;

@@ -6,12 +6,14 @@ namespace awq {
 
 // Prepared activations: x' = x inv_s[k] 2^p as fp16, one rounding, p such that the row's largest
 // |x inv_s| lies in [2^14, 2^15) (a value 2^-29 of that and more keeps all of its bits; a row with
-// an infinity or a NaN is taken as it is, p = 0), and the row's factor 2^-p. bf16 activations
-// become fp16 without a loss that a product could notice, and nothing overflows. One CTA per row.
+// an infinity or a NaN is taken as it is, p = 0), and the row's factor 2^-p. Every finite fp32
+// row has such a p, so nothing overflows; from 2^-113 of the largest down p stays at 126, where both
+// powers are normal numbers and a bf16 value of any size is an fp16 one. One CTA per row.
 //  * kFragments, for the streaming kernel (gemv_fused.cuh): chunks of chunk_groups groups, each
 //    group [8-k chunk j][32-k quarter c] of 8 values as the MMA fragments are read, then the
-//    groups' sums of x' times 2^-24; the factor is times 2^24 (the codes come in as q 2^-24). With
-//    split = 1 a row is two: x' rounded, then the rounding's remainder, rounded.
+//    groups' sums of x' times 2^-24 (the codes come in as q 2^-24; the kernel takes that off, since
+//    a factor times 2^24 could leave fp32's range). With split = 1 a row is two: x' rounded, then
+//    the rounding's remainder, rounded.
 //  * else plain rows [T, K], for the tensor-core kernel (gemm_fused.cuh).
 // The factors [T] follow the rows.
 constexpr int kPrepThreads = 256;
@@ -91,9 +93,9 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_rows_kernel(
   finite = __syncthreads_and(finite);
 #pragma unroll
   for (int w = 0; w < kPrepThreads / 32; ++w) big = fmaxf(big, part[w]);
-  // 2^14 <= big 2^p < 2^15, from big's exponent; |p| <= 100 keeps both factors normal numbers
+  // 2^14 <= big 2^p < 2^15, from big's exponent: p >= -113, and up to 126 both powers are normal
   int p = finite && big > 0.0f ? 14 - (static_cast<int>(__float_as_uint(big) >> 23) - 127) : 0;
-  p = p > 100 ? 100 : p < -100 ? -100 : p;
+  p = p > 126 ? 126 : p;
   const float up = __uint_as_float(static_cast<uint32_t>(127 + p) << 23);
   const int64_t row_bytes = static_cast<int64_t>(chunks) * chunk_bytes;
   uint8_t* base = out + (static_cast<int64_t>(row) << split) * row_bytes;
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_rows_kernel(
     const int64_t rows_bytes =
         kFragments ? (static_cast<int64_t>(T) << split) * row_bytes : static_cast<int64_t>(T) * K * 2;
     reinterpret_cast<float*>(out + rows_bytes)[row] =
-        __uint_as_float(static_cast<uint32_t>(127 - p) << 23) * (kFragments ? 16777216.0f : 1.0f);
+        __uint_as_float(static_cast<uint32_t>(127 - p) << 23);
   }
 }
 
