@@ -4,7 +4,10 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_experts import BF16, F16, Layer, awq, cu, dense, tokens  # noqa: F401 (awq: fixture)
+import oracle as O
+from expert_reference import TINY, U, f64
+from test_gpu_experts import (BF16, F16, Layer, awq, cu, dense, grouped, offsets_of,  # noqa: F401
+                              tokens)   # (awq: fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +81,49 @@ def test_a_row_of_each_size_beside_the_others(awq):  # noqa: F811
         want = dense(awq, layer, X)
         assert torch.equal(y.double() * down, want.double())
         assert (y[-1] == 0).all()
+
+
+def output_rounding_alone(layer, e, X):
+    """(y, bound of one output, the norm that the rounding to y's type leaves) of expert e's product
+    where nothing but the output is rounded to 16 bits: codes, scales, zero points, x and x * inv_s
+    enter in fp32 or exactly. The sums of q x and of z x are apart, so their fp32 roundings (one a
+    16-wide step, the joins across groups and warps) go by |x| (q + z) scale; two-part x * inv_s
+    adds 2^-22 of that."""
+    qw, sc, z = layer.host[e]
+    scale, zero = (np.repeat(v.astype(np.float64).T, 128, axis=1) for v in (sc, z))
+    q = O.unpack(qw, layer.bits, layer.K).astype(np.float64)
+    x = f64(X) if layer.inv is None else f64(X) * f64(layer.inv[e])[None, :]
+    y = x @ ((q - zero) * scale).T
+    size = np.abs(x) @ ((q + zero) * scale).T
+    u, t = U[layer.dtype], layer.dtype
+    tol = ((layer.K / 16 + 32) * 2.0 ** -23 + 2.0 ** -22) * size
+    rounded = f64(torch.from_numpy(y).to(t))
+    return y, tol + u * (np.abs(y) + tol) + TINY[t], np.linalg.norm(rounded - y)
+
+
+def assert_rounded_once(got, want, tol, left):
+    """Each output within its bound, and the whole within 2 % of the rounding's own norm: of the fp32
+    roundings, each group's are some 2^-23 sqrt(128 * 8) |x| q scale, which over all groups is
+    below a hundredth of fp16's 2^-11 of the output."""
+    got = f64(got)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= tol).all()
+    norm = np.linalg.norm(got - want)
+    assert norm <= 1.02 * left, (norm / left, norm / np.linalg.norm(want))
+
+
+# the decode kernel (one token; more), then the streaming kernel (N odd; with inv_s: two parts a token)
+@pytest.mark.parametrize("M,N,K,bits,dtype,inv", [
+    (1, 4096, 4096, 4, F16, False), (1, 2048, 2176, 3, F16, False), (1, 1024, 384, 4, F16, False),
+    (2, 2048, 4096, 4, F16, False), (8, 512, 1024, 3, F16, False), (1, 2001, 2176, 4, F16, False),
+    (7, 333, 1024, 3, F16, False), (1, 4096, 4096, 4, F16, True), (3, 1001, 2176, 3, F16, True),
+    (4, 512, 1024, 4, F16, True), (1, 4096, 4096, 4, BF16, False), (5, 1001, 1024, 4, BF16, False)])
+@pytest.mark.parametrize("e", [0, -6, -12])
+def test_few_rows_are_rounded_once(awq, M, N, K, bits, dtype, inv, e):  # noqa: F811
+    """Up to 8 rows nothing is rounded to 16 bits before the output, small activations included."""
+    rng = np.random.default_rng([M, N, K, bits])
+    layer = Layer(rng, 1, N, K, bits, dtype, inv)
+    X = tokens(rng, M, K, dtype) * 2.0 ** e
+    y = dense(awq, layer, X)
+    awq.awq_check_error()
+    assert_rounded_once(y, *output_rounding_alone(layer, 0, X))

@@ -339,6 +339,26 @@ __device__ __forceinline__ void raw3_chunk(uint32_t w0, uint32_t w1, uint32_t w2
   }
 }
 
+// The pairs (k0, k1), (k2, k3), (k4, k5), (k6, k7) of a 4-bit word as fp16 subnormals:
+// q 2^-24, q 2^-20, q 2^-24, q 2^-20.
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&v)[4]) {
+  v[0] = w & 0x000F000Fu;
+  v[1] = w & 0x00F000F0u;
+  v[2] = (w >> 8) & 0x000F000Fu;
+  v[3] = (w >> 8) & 0x00F000F0u;
+}
+// 3 bits: the pairs of 8-k chunk i of a 32-k block (words as in raw3_chunk), all q 2^-24.
+__device__ __forceinline__ void code3_pairs(uint32_t w0, uint32_t w1, uint32_t w2, int i,
+                                            uint32_t (&v)[4]) {
+  const uint32_t wlo = i < 2 ? w0 : w1;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int pp = 4 * (i & 1) + e, hb = 4 * i + e;
+    const uint32_t hs = hb >= 2 ? (w2 >> (hb - 2)) : (w2 << (2 - hb));
+    v[e] = lop3_and_or(hs, 0x00040004u, (wlo >> (2 * pp)) & 0x00030003u);
+  }
+}
+
 // The exact pairs (q - z) in bf16: the raw pairs minus (128 + z).
 __device__ __forceinline__ void dequant_word_qz_bf16(uint32_t w, uint32_t bias, uint32_t (&out)[4]) {
   raw_word<true>(w, out);
@@ -346,7 +366,15 @@ __device__ __forceinline__ void dequant_word_qz_bf16(uint32_t w, uint32_t bias, 
   for (int i = 0; i < 4; ++i) out[i] = b2_as_u32(__hsub2(u32_as_b2(out[i]), u32_as_b2(bias)));
 }
 
-// kFused: Y goes through the fused epilogue (bias, activation, product, sum) as it is stored.
+// kFused: Y goes through the fused epilogue (bias, activation, product, sum) as it is stored. One
+// fp16 token then takes the codes as subnormals, q 2^-24 and, of the pairs four bits higher, q 2^-20
+// (code_pairs): as many instructions as with the offset of 1024, but X stays undivided (a value below
+// 2^-10 over 16 may lose bits in fp16), and no sum of 1024 x is taken off again. The two kinds go to
+// MMAs of their own and meet in fp32. A row of magnitude 1e-4 was off by 5.5e-4 of the output's norm
+// with the division and is off by 2.1e-4, the output's rounding, without it; us a call in a graph, with
+// the offset and without: [4096, 4096] 4.62 and 4.62, [11008, 4096] 9.55 and 9.73, [4096, 11008] 9.83
+// and 9.82, 3 bits [4096, 4096] 6.06 and 6.00. (The product without an epilogue keeps the form that
+// it had, and its results.)
 template <int kNTiles, bool kOffset, bool kBf16 = false, int kBits = 4, bool kFused = false>
 __global__ void __launch_bounds__(kG4Threads, 2) gemv_stream_kernel(
     const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_s,
@@ -361,7 +389,8 @@ __global__ void __launch_bounds__(kG4Threads, 2) gemv_stream_kernel(
   constexpr uint32_t kTx = kGemvRows * kRowW * 4 + kG4SBytes + kG4ZBytes;
   // M = 1 with fp16 and 4 bits stages columns k%8 in {2,3,6,7} divided by 16 (the nibbles
   // stored 4 bits higher come out as 1024 + 16q); every other form has one raw pair form
-  constexpr bool kDiv16 = !kBf16 && kBits == 4;
+  constexpr bool kSub = kFused && kOffset && !kBf16;
+  constexpr bool kDiv16 = !kBf16 && kBits == 4 && !kSub;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -518,9 +547,10 @@ __global__ void __launch_bounds__(kG4Threads, 2) gemv_stream_kernel(
             c2 += __shfl_xor_sync(0xffffffffu, c2, o);
           }
           if (ch == 0 && live) {
-            // C1 = base * sum of the staged values (c1 == c2 unless kDiv16)
-            cc[(g * kTok + m) * 2] = kBf16 ? 128.0f * c2 : 1024.0f * c1;
-            cc[(g * kTok + m) * 2 + 1] = c2;
+            // C1 = base * sum of the staged values (c1 == c2 unless kDiv16); kSub: no base, and the
+            // codes' 2^-24, which the tile's end takes off
+            cc[(g * kTok + m) * 2] = kBf16 ? 128.0f * c2 : kSub ? 0.0f : 1024.0f * c1;
+            cc[(g * kTok + m) * 2 + 1] = kSub ? c2 * 5.9604644775390625e-8f : c2;
           }
         }
       }
@@ -621,7 +651,13 @@ __global__ void __launch_bounds__(kG4Threads, 2) gemv_stream_kernel(
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t va[4], vb[4];
-          if constexpr (kBits == 3) {
+          if constexpr (kSub && kBits == 3) {
+            code3_pairs(wA[q].x, wA[q].y, wA[q].z, j, va);
+            code3_pairs(wB[q].x, wB[q].y, wB[q].z, j, vb);
+          } else if constexpr (kSub) {
+            code_pairs(wordsA[j], va);
+            code_pairs(wordsB[j], vb);
+          } else if constexpr (kBits == 3) {
             raw3_chunk<kBf16>(wA[q].x, wA[q].y, wA[q].z, j, va);
             raw3_chunk<kBf16>(wB[q].x, wB[q].y, wB[q].z, j, vb);
             if (!kOffset) {   // minus the bias pair (1024 + z) / (128 + z): the exact q - z
@@ -654,17 +690,28 @@ __global__ void __launch_bounds__(kG4Threads, 2) gemv_stream_kernel(
             uint4 xv = make_uint4(0u, 0u, 0u, 0u);
             if (m < M && AWQ_IN_BOUNDS(((g * 4 + j) * M + m) * 4 + c < G * 4 * M * 4))
               xv = reinterpret_cast<const uint4*>(xs)[((g * 4 + j) * M + m) * 4 + c];
-            const uint32_t a0[4] = {va[0], vb[0], va[1], vb[1]};
-            mma_16816<kBf16>(acc[t][j], a0, xv.x, xv.y);
-            const uint32_t a1[4] = {va[2], vb[2], va[3], vb[3]};
-            mma_16816<kBf16>(acc[t][j], a1, xv.z, xv.w);
+            if constexpr (kSub && kBits == 4) {   // q 2^-24 in acc 0 and 1, q 2^-20 in 2 and 3
+              const uint32_t a0[4] = {va[0], vb[0], va[2], vb[2]};
+              mma_16816<kBf16>(acc[t][j >> 1], a0, xv.x, xv.z);
+              const uint32_t a1[4] = {va[1], vb[1], va[3], vb[3]};
+              mma_16816<kBf16>(acc[t][2 + (j >> 1)], a1, xv.y, xv.w);
+            } else {
+              const uint32_t a0[4] = {va[0], vb[0], va[1], vb[1]};
+              mma_16816<kBf16>(acc[t][j], a0, xv.x, xv.y);
+              const uint32_t a1[4] = {va[2], vb[2], va[3], vb[3]};
+              mma_16816<kBf16>(acc[t][j], a1, xv.z, xv.w);
+            }
           }
         }
 #pragma unroll
         for (int t = 0; t < kNTiles; ++t) {
           float d[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) d[i] = (acc[t][0][i] + acc[t][1][i]) + (acc[t][2][i] + acc[t][3][i]);
+          for (int i = 0; i < 4; ++i) {
+            const float s01 = acc[t][0][i] + acc[t][1][i], s23 = acc[t][2][i] + acc[t][3][i];
+            if constexpr (kSub) d[i] = fmaf(kBits == 4 ? 0.0625f : 1.0f, s23, s01);
+            else d[i] = s01 + s23;
+          }
           if (kOffset && AWQ_IN_BOUNDS((g * kTok + 8 * t + 2 * c) * 2 + 4 <= G * kTok * 2)) {
             const float zA = static_cast<float>(zAi[q]), zB = static_cast<float>(zBi[q]);
             const float4 cm = *reinterpret_cast<const float4*>(cc + (g * kTok + 8 * t + 2 * c) * 2);
@@ -705,7 +752,7 @@ __global__ void __launch_bounds__(kG4Threads, 2) gemv_stream_kernel(
         const int m0 = 8 * t + 2 * c, m1 = m0 + 1;
         if constexpr (kFused) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = fin.apply(epi, v[i], i);
+          for (int i = 0; i < 4; ++i) v[i] = fin.apply(epi, kSub ? v[i] * 16777216.0f : v[i], i);
         }
         if (nA < N && AWQ_IN_BOUNDS(tile < t1)) {
           if (m0 < M) Y[static_cast<int64_t>(m0) * N + nA] = float_to_act<kBf16>(v[0]);

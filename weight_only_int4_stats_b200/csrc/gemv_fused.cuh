@@ -127,25 +127,6 @@ __device__ __forceinline__ void lds128(uint32_t (&v)[4], uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
 }
-// The pairs (k0, k1), (k2, k3), (k4, k5), (k6, k7) of a 4-bit word as fp16 subnormals:
-// q 2^-24, q 2^-20, q 2^-24, q 2^-20.
-__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&v)[4]) {
-  v[0] = w & 0x000F000Fu;
-  v[1] = w & 0x00F000F0u;
-  v[2] = (w >> 8) & 0x000F000Fu;
-  v[3] = (w >> 8) & 0x00F000F0u;
-}
-// 3 bits: the pairs of 8-k chunk i of a 32-k block (words as in raw3_chunk), all q 2^-24.
-__device__ __forceinline__ void code3_pairs(uint32_t w0, uint32_t w1, uint32_t w2, int i,
-                                            uint32_t (&v)[4]) {
-  const uint32_t wlo = i < 2 ? w0 : w1;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int pp = 4 * (i & 1) + e, hb = 4 * i + e;
-    const uint32_t hs = hb >= 2 ? (w2 >> (hb - 2)) : (w2 << (2 - hb));
-    v[e] = lop3_and_or(hs, 0x00040004u, (wlo >> (2 * pp)) & 0x00030003u);
-  }
-}
 __device__ __forceinline__ float lds32f(uint32_t addr) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
