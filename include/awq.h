@@ -248,11 +248,12 @@ AWQ_API awq_status awq_gemm_w4a16(const awq_f16* X, int64_t M, const uint32_t* q
  * mul or residual may be Y itself (each output is read before it is written, by the same
  * thread); apart from that Y overlaps no input. The other arguments, the flags and the
  * no-ops are awq_gemm_w4a16's.
- * Roundings before the output's: up to 8 rows none, with inv_s in fp16 too (x * inv_s is held in
- * two fp16 parts), while bf16 activations times inv_s are rounded once to fp16's 11 bits, scaled
- * by a power of two per row; more rows take the weights as fp16, (q - z) * scale rounded once
- * (times inv_s[k] before that rounding, for fp16 activations). A row of X that holds an infinity
- * or a NaN gives infinities or NaN, which of the two is not specified; other rows do not notice.
+ * Roundings before the output's: with up to 8 rows none, sums are fp32 (x * inv_s is held in two
+ * fp16 parts for fp16 activations; for bf16 ones it is rounded once to fp16's 11 bits, scaled by a
+ * power of two per row, and one bf16 row without inv_s goes through sums of (128 + q) x, which are
+ * finite below 2^112). More rows take the weights as fp16: (q - z) * scale rounded once (times
+ * inv_s[k] before that rounding, for fp16 activations). A row of X that holds an infinity or a
+ * NaN gives infinities or NaN, which of the two is not specified; other rows do not notice.
  * workspace: at least awq_gemm_epilogue_workspace_size(M, N, K, bits, inv_s != NULL, flags)
  * bytes. */
 #define AWQ_ACT_NONE 0
@@ -281,7 +282,9 @@ AWQ_API awq_status awq_gemm_w4a16_epilogue(
  * awq_gemm_w4a16_grouped: awq_gemm_w4a16_epilogue's product, each row against its expert's
  * packed weight: qweight [E, N, K/8] (or [E, N, 3K/32]), scales [E, K/128, N], zeros
  * [E, K/128, N], inv_s NULL or [E, K], bias NULL or [E, N]; mul, residual, Y [T, N]. Only the
- * weights of experts with rows are read. E * N and E * N * K / 128 must be below 2^31. workspace: at least
+ * weights of experts with rows are read. Its roundings are those of awq_gemm_w4a16_epilogue's calls
+ * with up to 8 rows where T <= 8 E, and of those with more where T > 8 E, however the rows are
+ * spread. E * N and E * N * K / 128 must be below 2^31. workspace: at least
  * awq_gemm_grouped_workspace_size(T, E, N, K, bits, inv_s != NULL, flags) bytes. */
 AWQ_API size_t awq_gemm_grouped_workspace_size(int64_t T, int64_t E, int64_t N, int64_t K, int bits,
                                                int with_inv_s, unsigned flags);

@@ -117,7 +117,8 @@ def assert_rounded_once(got, want, tol, left):
     (1, 4096, 4096, 4, F16, False), (1, 2048, 2176, 3, F16, False), (1, 1024, 384, 4, F16, False),
     (2, 2048, 4096, 4, F16, False), (8, 512, 1024, 3, F16, False), (1, 2001, 2176, 4, F16, False),
     (7, 333, 1024, 3, F16, False), (1, 4096, 4096, 4, F16, True), (3, 1001, 2176, 3, F16, True),
-    (4, 512, 1024, 4, F16, True), (1, 4096, 4096, 4, BF16, False), (5, 1001, 1024, 4, BF16, False)])
+    (4, 512, 1024, 4, F16, True), (1, 4096, 4096, 4, BF16, False), (5, 1001, 1024, 4, BF16, False),
+    (5, 1001, 2176, 4, F16, True), (6, 4096, 1024, 3, F16, True), (8, 512, 4096, 4, F16, True)])
 @pytest.mark.parametrize("e", [0, -6, -12])
 def test_few_rows_are_rounded_once(awq, M, N, K, bits, dtype, inv, e):  # noqa: F811
     """Up to 8 rows nothing is rounded to 16 bits before the output, small activations included."""
@@ -127,3 +128,23 @@ def test_few_rows_are_rounded_once(awq, M, N, K, bits, dtype, inv, e):  # noqa: 
     y = dense(awq, layer, X)
     awq.awq_check_error()
     assert_rounded_once(y, *output_rounding_alone(layer, 0, X))
+
+
+@pytest.mark.parametrize("counts,N,K,bits,dtype,inv", [
+    ([1] * 24, 512, 1024, 4, F16, True), ([1] * 24, 500, 2176, 3, F16, False),
+    ([0, 2, 0, 1, 5, 0, 1, 1], 512, 1024, 4, F16, False), ([8, 7, 9, 5], 300, 1024, 4, F16, True),
+    ([30, 0, 1, 0], 512, 384, 3, F16, True), ([1, 0, 0, 2], 512, 2048, 4, BF16, False),
+    ([4] * 12, 512, 1024, 3, BF16, False)])
+def test_experts_of_few_rows_are_rounded_once(awq, counts, N, K, bits, dtype, inv):  # noqa: F811
+    """Up to 8 rows an expert on average, however they are spread; the norm is taken over the
+    whole call, so that experts of one row count in it."""
+    rng = np.random.default_rng([N, K, len(counts)])
+    layer = Layer(rng, len(counts), N, K, bits, dtype, inv)
+    off = offsets_of(counts, 0)
+    X = tokens(rng, int(off[-1]), K, dtype)
+    y = grouped(awq, layer, X, off)
+    awq.awq_check_error()
+    each = [output_rounding_alone(layer, e, X[off[e]:off[e + 1]]) for e in range(len(counts))
+            if counts[e]]
+    want, tol = (np.concatenate([v[i] for v in each]) for i in range(2))
+    assert_rounded_once(y, want, tol, np.sqrt(sum(v[2] ** 2 for v in each)))
