@@ -26,3 +26,48 @@ def test_up_to_8_fp16_rows_with_inv_s_are_held_in_two_parts(L, N, K, bits):
         for T in (1, 4 * E, 4 * E + 1, 8 * E):
             assert L.awq_gemm_grouped_workspace_size(T, E, N, K, bits, 1, 0) >= T * 4 * K
         assert L.awq_gemm_grouped_workspace_size(8 * E + 1, E, N, K, bits, 1, 0) == 0
+
+
+class Devices:
+    """A machine of unlike GPUs: the library's size query goes by the current device."""
+
+    def __init__(self, awq, monkeypatch):
+        self.current, self.calls, self.allocated = 0, [], []
+        monkeypatch.setattr(awq, "lib", lambda: self)
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: self.current)
+        monkeypatch.setattr(torch.cuda, "device", self.guard)
+        monkeypatch.setattr(awq, "_current_raw_stream", lambda index: 0)
+        monkeypatch.setattr(awq, "_new", self.new)
+
+    def guard(self, index):
+        class Guard:
+            def __enter__(g):
+                g.before, self.current = self.current, index
+
+            def __exit__(g, *exc):
+                self.current = g.before
+        return Guard()
+
+    def new(self, nbytes, dtype, index, stream):
+        self.allocated.append((index, nbytes))
+
+        class Memory:
+            get_device, is_contiguous = (lambda m: index), (lambda m: True)
+            data_ptr, numel, element_size = (lambda m: 256), (lambda m: nbytes), (lambda m: 1)
+        return Memory()
+
+    def awq_size(self, n):
+        return n * (self.current + 1)
+
+    def awq_op(self, x, ws, ws_bytes, stream):
+        self.calls.append((self.current, x, ws_bytes))
+        return 0 if ws_bytes >= x * (self.current + 1) else 3
+
+
+def test_binding_plans_for_the_tensors_device(monkeypatch):
+    import weight_only_int4_stats_b200 as awq
+    box = Devices(awq, monkeypatch)
+    for index in (1, 0, 1, 3):   # not the current device, and the same sizes on each
+        awq._call("awq_op", index, None, ("awq_size", 100), None, (100,))
+        assert box.allocated[-1] == (index, 100 * (index + 1))
+        assert box.calls[-1] == (index, 100, 100 * (index + 1)) and box.current == 0

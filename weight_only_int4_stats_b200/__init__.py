@@ -320,23 +320,26 @@ def _new(shape, dtype, device, stream):
 
 
 @functools.lru_cache(maxsize=4096)
-def _workspace_bytes(L, fn, *sizes):
+def _workspace_bytes(L, index, fn, *sizes):
+    """The size query `fn` of device `index`, which is the current one: the library plans a call
+    for the current device's SMs."""
     return getattr(L, fn)(*sizes)
 
 
-def _call(fn, index, stream, need, workspace, args):
-    """Calls the C entry point `fn` with `args`, then (workspace, its bytes) unless need is
-    None, then the stream; on the inputs' device, with scratch memory that belongs to the
-    stream that uses it."""
+def _call(fn, index, stream, query, workspace, args):
+    """Calls the C entry point `fn` with `args`, then (workspace, its bytes) unless query (the size
+    query and its arguments) is None, then the stream; on the inputs' device, with scratch memory
+    that belongs to the stream that uses it."""
     if index < 0:
         raise TypeError(f"{fn}: expected CUDA tensors")
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
-            return _call(fn, index, stream, need, workspace, args)
-    if need is not None:
+            return _call(fn, index, stream, query, workspace, args)
+    if query is not None:
         ws = workspace
-        if ws is None and need > 0:
-            ws = _new(need, torch.uint8, index, stream)
+        if ws is None:
+            need = _workspace_bytes(lib(), index, *query)
+            ws = _new(need, torch.uint8, index, stream) if need > 0 else None
         if ws is None:
             args += (None, 0)
         else:
@@ -377,8 +380,7 @@ def awq_gemm_w4a16_epilogue(X: torch.Tensor, qweight: torch.Tensor, scales: torc
     flags = (WEIGHTS_READY if weights_ready else 0) | (BF16 if t is torch.bfloat16 else 0)
     Y = _new((M, N), t, X.device, stream) if out is None else out
     _call("awq_gemm_w4a16_epilogue", dev, stream,
-          _workspace_bytes(lib(), "awq_gemm_epilogue_workspace_size", M, N, K, bits,
-                           inv_s is not None, flags), workspace,
+          ("awq_gemm_epilogue_workspace_size", M, N, K, bits, inv_s is not None, flags), workspace,
           (x, M, _arg(qweight, torch.int32, (N, packed_words_per_row(K, bits)), dev, "qweight"),
            _arg(scales, torch.float16, (G, N), dev, "scales"),
            _arg(zeros, torch.uint8, (G, N), dev, "zeros"), N, K, bits, group,
@@ -410,8 +412,7 @@ def awq_gemm_w4a16_grouped(X: torch.Tensor, offsets: torch.Tensor, qweight: torc
     flags = (WEIGHTS_READY if weights_ready else 0) | (BF16 if t is torch.bfloat16 else 0)
     Y = _new((T, N), t, X.device, stream) if out is None else out
     _call("awq_gemm_w4a16_grouped", dev, stream,
-          _workspace_bytes(lib(), "awq_gemm_grouped_workspace_size", T, E, N, K, bits,
-                           inv_s is not None, flags), workspace,
+          ("awq_gemm_grouped_workspace_size", T, E, N, K, bits, inv_s is not None, flags), workspace,
           (x, T, _arg(offsets, torch.int32, (E + 1,), dev, "offsets"), E,
            _arg(qweight, torch.int32, (E, N, packed_words_per_row(K, bits)), dev, "qweight"),
            _arg(scales, torch.float16, (E, G, N), dev, "scales"),
@@ -433,7 +434,7 @@ def awq_act_stats_grouped(X: torch.Tensor, offsets: torch.Tensor,
     dev, (T, K), E = X.get_device(), X.shape, offsets.numel() - 1
     s_x = _new((E, K), torch.float32, X.device, stream) if out is None else out
     _call("awq_act_stats_grouped", dev, stream,
-          _workspace_bytes(lib(), "awq_act_stats_grouped_workspace_size", T, E, K), workspace,
+          ("awq_act_stats_grouped_workspace_size", T, E, K), workspace,
           (_arg(X, torch.float16, (T, K), dev, "X"), T,
            _arg(offsets, torch.int32, (E + 1,), dev, "offsets"), E, K,
            _arg(s_x, torch.float32, (E, K), dev, "out")))
