@@ -5,9 +5,9 @@ import pytest
 import torch
 
 import oracle as O
-from expert_reference import TINY, U, f64
+from expert_reference import TINY, U, assert_within, f64
 from test_gpu_experts import (BF16, F16, Layer, awq, cu, dense, grouped, offsets_of,  # noqa: F401
-                              tokens)   # (awq: fixture)
+                              silu_mul_tolerance, tokens)   # (awq: fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -148,3 +148,59 @@ def test_experts_of_few_rows_are_rounded_once(awq, counts, N, K, bits, dtype, in
             if counts[e]]
     want, tol = (np.concatenate([v[i] for v in each]) for i in range(2))
     assert_rounded_once(y, want, tol, np.sqrt(sum(v[2] ** 2 for v in each)))
+
+
+@pytest.mark.parametrize("M,N,K,bits,dtype,inv", [
+    (5, 67, 11008, 4, BF16, False), (3, 40, 14336, 3, F16, True), (40, 130, 8320, 4, BF16, True),
+    (33, 64, 16512, 3, BF16, False)])
+def test_rows_longer_than_the_preparation_keeps_in_registers(awq, M, N, K, bits, dtype, inv):  # noqa: F811
+    """K past 8192: the preparation reads the rest of a row twice. Its last part alone holds the
+    row's largest values in every second row, so both passes have to see it."""
+    rng = np.random.default_rng([M, N, K])
+    layer = Layer(rng, 1, N, K, bits, dtype, inv)
+    X = tokens(rng, M, K, dtype)
+    X[::2, 8192:] *= 64
+    y = dense(awq, layer, X)
+    awq.awq_check_error()
+    if M <= 8 and not (inv and dtype == BF16):
+        assert_rounded_once(y, *output_rounding_alone(layer, 0, X))
+    else:
+        want, tol = layer.want(0, X)
+        assert assert_within(y, want, tol) <= 3 * U[dtype]
+
+
+@pytest.mark.parametrize("M", [2, 5, 8])
+def test_product_without_parts_has_the_plain_products_bits(awq, M):  # noqa: F811
+    """From 2 rows to 8 both are the decode kernel with exact q - z (bf16: from one row on)."""
+    rng = np.random.default_rng(M)
+    for dtype, bits, rows in ((F16, 4, M), (F16, 3, M), (BF16, 4, M), (BF16, 4, 1)):
+        layer = Layer(rng, 1, 512, 1024, bits, dtype)
+        X = tokens(rng, rows, 1024, dtype)
+        plain = awq.awq_gemm_w4a16(X, layer.qw[0], layer.sc[0], layer.z[0], 512, 1024, bits)
+        assert torch.equal(dense(awq, layer, X), plain)
+
+
+@pytest.mark.parametrize("counts,I,K", [([3000, 0, 2900], 14336, 4096), ([2700, 40, 0, 1500], 2000, 1024)])
+def test_silu_mul_of_many_rows_an_expert(awq, counts, I, K):  # noqa: F811
+    """Token tiles of 256 rows: in tiles of 128 weight rows (long calls with a deep K) and of 64;
+    sampled outputs, every tile's and expert's borders among the rows."""
+    rng = np.random.default_rng([I, K])
+    E, off = len(counts), offsets_of(counts, 0)
+    X = tokens(rng, int(off[-1]), K, F16)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    Wg, Wu = (torch.randn(E, I, K, generator=g, device="cuda").mul_(K ** -0.5).to(F16) for _ in range(2))
+    h = awq.awq_silu_mul_gemm_grouped(X, cu(off), Wg, Wu)
+    awq.awq_check_error()
+    cols = cu(np.unique(np.concatenate([rng.integers(0, I, 200), [0, 63, 64, 127, 128, I - 1]])))
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        if a == b:
+            continue
+        at = np.concatenate([rng.integers(a, b, 60), [a, b - 1], np.arange(a + 255, b, 256),
+                             np.arange(a + 256, b, 256)])
+        rows = cu(np.unique(at))
+        want, tol = silu_mul_tolerance(X[rows], Wg[e][cols], Wu[e][cols])
+        got = h[rows][:, cols]
+        assert_within(got, want, tol, e)
+        # as a whole: fp16's rounding, and what fp32 sums of K / 16 steps add to it
+        assert np.linalg.norm(f64(got) - want) <= 1.05 * 2.0 ** -11 * 3 ** -0.5 * np.linalg.norm(want)
