@@ -182,8 +182,8 @@ def test_product_without_parts_has_the_plain_products_bits(awq, M):  # noqa: F81
 
 @pytest.mark.parametrize("counts,I,K", [([3000, 0, 2900], 14336, 4096), ([2700, 40, 0, 1500], 2000, 1024)])
 def test_silu_mul_of_many_rows_an_expert(awq, counts, I, K):  # noqa: F811
-    """Token tiles of 256 rows: in tiles of 128 weight rows (long calls with a deep K) and of 64;
-    sampled outputs, every tile's and expert's borders among the rows."""
+    """Token tiles of 256 rows with a deep and a short K; sampled outputs, every tile's and
+    expert's borders among the rows."""
     rng = np.random.default_rng([I, K])
     E, off = len(counts), offsets_of(counts, 0)
     X = tokens(rng, int(off[-1]), K, F16)

@@ -1139,18 +1139,20 @@ awq_status launch_gated_tiles(const void* X, const void* gate, const void* up, a
 }
 
 // Tiles for experts of few rows: 128 rows of both weights, or 64 where those take clearly fewer
-// rounds of the CTAs, counted with one token tile an expert and some more (us in tiles of 128 and
-// of 64: 1003 rows over 16 experts of [1536, 2048] 46 and 41, 2400 rows 90 and 72, 300 over 4 of
-// [2048, 4096] 35 and 30; but 1200 over 8 of [4096, 4096] 112 and 126, 8192 over 64 of
-// [1408, 2048] 154 and 174, where the rounds only double and X is read twice as often).
+// rounds of the CTAs, counted with one token tile an expert (us in tiles of 128 and of 64, rows
+// unevenly spread: 1003 rows over 16 experts of [1536, 2048] 44 and 39, 2400 rows 62 and 52, 634 over
+// 24 of [334, 1536] 16.4 and 12.6, 572 over 83 of [444, 3328] 88 and 78; but 1200 over 8 of
+// [4096, 4096] 115 and 129, 27 over 14 of [2456, 512] 12.2 and 16.2, 4241 over 38 of [1315, 5888]
+// 252 and 293, where the rounds only double and X is read twice as often). A twelfth more token
+// tiles in the count, for experts that need a second one, chose the slower side in 20 of the 23 drawn
+// shapes where it made a difference, by up to a third.
 template <int BN>
 awq_status launch_gated(const void* X, const void* gate, const void* up, const awq::FusedArgs& a,
                         cudaStream_t st) {
   const int64_t sms = num_sms();
   const int64_t active = a.M < a.E ? a.M : a.E;
-  const int64_t tokens = active + active / 12;
-  const int64_t whole = ((a.N + 127) / 128 * tokens + sms - 1) / sms;
-  const int64_t half = ((a.N + 63) / 64 * tokens + sms - 1) / sms;
+  const int64_t whole = ((a.N + 127) / 128 * active + sms - 1) / sms;
+  const int64_t half = ((a.N + 63) / 64 * active + sms - 1) / sms;
   return 10 * half < 16 * whole ? launch_gated_tiles<BN, true>(X, gate, up, a, st)
                                 : launch_gated_tiles<BN, false>(X, gate, up, a, st);
 }
@@ -1227,14 +1229,10 @@ awq_status awq_silu_mul_gemm_grouped(const awq_f16* X, int64_t T, const int32_t*
   if (rows <= 128) return launch_gated<128>(X, W_gate, W_up, args, st);
   if (rows <= 256) return launch_gated<256>(X, W_gate, W_up, args, st);
   // Many rows: tiles of 64, whose one accumulator leaves room for a second one, so that epilogues
-  // overlap; but of 128, which read X once, where a call is long enough for the power limit and K
-  // for the epilogues not to count (us in tiles of 128 and of 64: 4096 rows over 8 experts of
-  // [14336, 4096] 995 and 981, 32768 over 64 of [1536, 2048] 433 and 420, 8192 over 8 of
-  // [14336, 1024] 583 and 492; 16384 over 8 of [14336, 4096] 3455 and 3552, 32768 over 8 of
-  // [4096, 4096] 1888 and 1964).
-  const int64_t tiles = (args.N + 127) / 128 * (T / 256 + (T < E ? T : E) / 2);
-  if (K >= 4096 && tiles > 16 * num_sms())
-    return launch_gated_tiles<256, false>(X, W_gate, W_up, args, st);
+  // overlap (us in tiles of 128 and of 64, calls run for 0.3 s each in turn: 16384 rows over 8 experts
+  // of [14336, 4096] 3720 and 3587, 6144 rows 1673 and 1473, 16384 rows of one [11008, 4096] 2547 and
+  // 2427, 8192 over 8 of [14336, 1024] 678 and 461; the other way at the deepest K and many rows alone:
+  // 65536 over 8 of [4096, 8192] 7630 and 7913, 16384 rows 2095 and 2080).
   return launch_gated_tiles<256, true>(X, W_gate, W_up, args, st);
 }
 
