@@ -19,8 +19,10 @@ struct FusedEpi {
 };
 
 // act(v) in fp32. A NaN stays one (with relu too); silu and gelu as their formulas give it, the
-// tanh form by (1 + tanh u) / 2 = 1 / (1 + exp(-2u)). The fast exponential and division are within
-// a few fp32 roundings, and far out v / inf is the limit 0.
+// tanh form by (1 + tanh u) / 2 = 1 / (1 + exp(-2u)). The fast division is within 2 fp32 roundings, the
+// fast exponential of x within 2 + |1.17 x|: at most 106 of them, 2^-17 of the value, before the
+// exponential overflows at 88.7, and there v / inf is the limit 0 (from 2^126 on the fast division
+// gives it too: silu's -1e-36 of v < -87.3).
 __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
     case kActRelu: return v < 0.0f ? 0.0f : v;

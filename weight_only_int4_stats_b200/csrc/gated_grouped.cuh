@@ -4,9 +4,11 @@
 // Tensor-bound. One tile is 128 rows of both weights (two A tiles and two TMEM accumulators)
 // against up to BN tokens of one expert; units (expert, row tile, token tile) go round the
 // persistent CTAs in gemm_fused.cuh's order, and the whole MMA warp walks the issue loop.
-// Measured: 16384 rows over 8 experts of [14336, 4096] 3.45 to 3.65 ms, 1050 to 1115
-// TFLOP/s under the power limit; 1003 rows over 16 experts of [1536, 2048] 41 us, where 189 MB of
-// weights would take 29 us.
+// Measured: 16384 rows over 8 experts of [14336, 4096] 3.36 ms with even experts, 1147 TFLOP/s, and
+// 3.59 to 3.64 with uneven ones, run for long under the power limit; 1003 rows over 16 experts of
+// [1536, 2048] 39 to 41 us, where 189 MB of weights would take 29 us. The tensor pipe works 77 % of the
+// time in tiles of 64 (4096 rows over 4 experts of [4096, 4096], 201 us); the rest are the last round of
+// CTAs and the waits for stages, of which each CTA reads its own (3.1 GB through L2 there).
 //   warp 0       TMA producer of X and both weights, in stages of 64 k
 //   warp 1       TMEM allocator and MMA issuer
 //   warps 2, 3   idle
@@ -15,9 +17,9 @@
 //                epilogue: eight warps and the fast exponential and division keep that short)
 // kStack: 64 rows of each weight in one A tile of 128 (gate above up) and one accumulator, so that
 // there is room for a second one and the epilogue overlaps the next tile even with BN = 256, and
-// half as much work a tile fills the last round of CTAs better; X is read twice as often. The up
-// half of the accumulator lies in other warps' TMEM lanes than the gate half, so the warps of a
-// pair trade tokens through shared memory.
+// half as much work a tile fills the last round of CTAs better; X is read twice as often. Which
+// calls take it stands at the launch. The up half of the accumulator lies in other warps' TMEM
+// lanes than the gate half, so the warps of a pair trade tokens through shared memory.
 #pragma once
 #include "common.cuh"
 #include "fused.cuh"

@@ -9,8 +9,8 @@
 // group of weights costs shared memory a 32 KB write, a 32 KB read by the tensor core and, in
 // the packed reads, bank conflicts; with few tokens per weight that is what bounds it (1.7 TB/s
 // of packed weights at 16 to 64 tokens). Here a builder thread owns one weight row: it reads
-// the row's codes of a block without bank conflicts, dequantizes in registers and stores the
-// block's columns of its lane.
+// the row's codes of a block (at 4 bits without bank conflicts), dequantizes in registers and
+// stores the block's columns of its lane.
 //   warp 0       TMA producer of X
 //   warp 1       TMEM allocator and single-thread tcgen05.mma issuer
 //   warp 2       TMA producer of packed codes, prefetch of scales and zero points
@@ -31,15 +31,18 @@
 // of two per row (with inv_s already in), and the epilogue takes the row's factor off. bf16
 // weights would need (q - z) * scale in two bf16 parts to be rounded only once (19 operations a
 // word of 8 codes, 45 with inv_s, against 13), and the dequantization is what bounds this kernel.
-// Measured: 8 experts of [14336, 4096] with 128 rows 93 us, 2.6 TB/s of packed weights; with 2048
-// rows 279 us, 863 TFLOP/s; [14336, 4096] x 4096 tokens 425 us, 1130 TFLOP/s. Few rows: the
-// dequantization (13 operations a word of 8 codes; 24 at 3 bits) on 4 warps a scheduler, and
-// their barriers. Many rows, run for long: the 1000 W power limit, under which the SM clock falls to
-// 1.45 GHz (2.1 ms for 8 experts of [4096, 14336] with 16384 rows), and about 200 cycles a group
-// that the MMA issuer spends waiting and counting.
+// Measured: 8 experts of [14336, 4096] with 128 rows 93 us, 2.7 TB/s of packed weights; with 2048
+// rows 279 us, 863 TFLOP/s, in a short run and 329 run for long; [14336, 4096] x 4096 tokens 434 us,
+// 1110 TFLOP/s, short and 491 long, where the plain product takes 398 and 458 and, with bias and
+// gelu as two more passes, 578 and 647. Few rows: the dequantization (13 operations a word of 8
+// codes; 24 at 3 bits) on 4 warps a scheduler, and their barriers. Many rows: the tensor pipe works
+// 58 % of the time (4096 tokens), since a group's weights are dequantized again for every 192 tokens,
+// the MMA issuer spends about 200 cycles a group waiting and counting, and each CTA reads its own X;
+// run for long, the 1000 W power limit takes the SM clock to 1.45 GHz besides (2.2 ms for 8 experts
+// of [4096, 14336] with 16384 rows).
 // Packed codes: 4 bits: boxes of 128 rows x 128 bytes (two groups) with the 128-byte swizzle;
-// 3 bits: one box of 3 or 5 groups (an odd multiple of 48 bytes per row, so that the 16-byte
-// reads of eight consecutive rows fall into eight different bank groups as they are).
+// 3 bits: one box of 3 or 5 groups (an odd multiple of 48 bytes per row: eight consecutive rows begin
+// in eight different bank groups, but the 8-byte reads of sixteen rows at once meet two to a bank).
 #pragma once
 #include "common.cuh"
 #include "fused.cuh"
@@ -224,7 +227,9 @@ __device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
 // operand pairs: exact q - z, then the scale with one rounding to fp16; with inv_s (this
 // quarter's) scale * inv_s[k] in fp32 and the product rounded once. (A factor rounded to fp16
 // before the product would make three roundings with the output's, sqrt(3) of one, where this
-// has sqrt(2).)
+// has sqrt(2): 2.9e-4 of an fp16 output's norm against 2.1e-4 of the output's rounding alone. The
+// MMA takes 16-bit operands: a weight of more bits would be two of them, and twice the dequantization
+// and MMAs. Under a bf16 output, rounded at 2^-9, an fp16 weight's 2^-12 does not show.)
 template <int kBits, bool kInv>
 __device__ __forceinline__ void dequant32(const uint32_t* w, uint32_t z, uint32_t sc, float scf,
                                           const float* inv, uint32_t (&o)[16]) {

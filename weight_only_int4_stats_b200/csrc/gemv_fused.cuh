@@ -23,9 +23,9 @@
 //    row, so no CTA waits to stage X and X may be of any length.
 //  * Scales and zero points are read from global memory one unit ahead (the producer warp
 //    prefetches them to L2 a ring's depth ahead), so N may be any number.
-// Measured on 8 experts of [14336, 4096], 4 rows each: 58.7 us, 4.2 TB/s of packed weights (the
-// ring alone, without the arithmetic, streams about 5.3); 128 experts of [1536, 2048] with 128 rows in
-// all, 37.5 us behind their preparation, 3.5 TB/s. Issue slots are half used: what is left is the
+// Measured on 8 experts of [14336, 4096], 4 rows each: 57.7 us, 4.3 TB/s of packed weights (the
+// ring alone, without the arithmetic, streams about 5.3); 128 experts of [1536, 2048], 128 rows on 80 of
+// them, 37.8 us with their preparation, 3.5 TB/s. Issue slots are half used: what is left is the
 // latency of a consumer warp's chain, four warps a scheduler, and some 200 integer operations a
 // unit that are not masks. Subtracting the zero point per weight instead took 47 us in the second
 // case, units half as large 49 us, and a load converted where it is issued (the warp then waits

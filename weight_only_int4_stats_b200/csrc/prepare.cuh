@@ -8,7 +8,9 @@ namespace awq {
 // |x inv_s| lies in [2^14, 2^15) (a value 2^-29 of that and more keeps all of its bits; a row with
 // an infinity or a NaN is taken as it is, p = 0), and the row's factor 2^-p. Every finite fp32
 // row has such a p, so nothing overflows; from 2^-113 of the largest down p stays at 126, where both
-// powers are normal numbers and a bf16 value of any size is an fp16 one. One CTA per row.
+// powers are normal numbers and a bf16 value of any size is an fp16 one. (x inv_s of a bf16 row is
+// rounded to 11 bits here; its output to 8, beside which that does not show, so it takes no
+// second part.) One CTA per row.
 //  * kFragments, for the streaming kernel (gemv_fused.cuh): chunks of chunk_groups groups, each
 //    group [8-k chunk j][32-k quarter c] of 8 values as the MMA fragments are read, then the
 //    groups' sums of x' times 2^-24 (the codes come in as q 2^-24; the kernel takes that off, since
