@@ -252,8 +252,10 @@ AWQ_API awq_status awq_gemm_w4a16(const awq_f16* X, int64_t M, const uint32_t* q
  * fp16 parts for fp16 activations; for bf16 ones it is rounded once to fp16's 11 bits, scaled by a
  * power of two per row, and one bf16 row without inv_s goes through sums of (128 + q) x, which are
  * finite below 2^112). More rows take the weights as fp16: (q - z) * scale rounded once (times
- * inv_s[k] before that rounding, for fp16 activations). A row of X that holds an infinity or a
- * NaN gives infinities or NaN, which of the two is not specified; other rows do not notice.
+ * inv_s[k] before that rounding, for fp16 activations). bf16 activations, and any with up to 8 rows,
+ * may become fp16 scaled by their row's power of two on the way, where a value below 2^-29 of the
+ * row's largest is held to 2^-39 of that. A row of X that holds an infinity or a NaN gives
+ * infinities or NaN, which of the two is not specified; other rows do not notice.
  * workspace: at least awq_gemm_epilogue_workspace_size(M, N, K, bits, inv_s != NULL, flags)
  * bytes. */
 #define AWQ_ACT_NONE 0
