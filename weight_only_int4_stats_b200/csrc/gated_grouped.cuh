@@ -5,7 +5,7 @@
 // against up to BN tokens of one expert; units (expert, row tile, token tile) go round the
 // persistent CTAs in gemm_fused.cuh's order, and the whole MMA warp walks the issue loop.
 // Measured: 16384 rows over 8 experts of [14336, 4096] 3.36 ms with even experts, 1147 TFLOP/s, and
-// 3.59 to 3.64 with uneven ones, run for long under the power limit; 1003 rows over 16 experts of
+// 3.51 to 3.64 with uneven ones, run for long under the power limit; 1003 rows over 16 experts of
 // [1536, 2048] 39 to 41 us, where 189 MB of weights would take 29 us. The tensor pipe works 77 % of the
 // time in tiles of 64 (4096 rows over 4 experts of [4096, 4096], 201 us); the rest are the last round of
 // CTAs and the waits for stages, of which each CTA reads its own (3.1 GB through L2 there).
