@@ -71,3 +71,12 @@ def test_binding_plans_for_the_tensors_device(monkeypatch):
         awq._call("awq_op", index, None, ("awq_size", 100), None, (100,))
         assert box.allocated[-1] == (index, 100 * (index + 1))
         assert box.calls[-1] == (index, 100, 100 * (index + 1)) and box.current == 0
+
+
+def test_plain_products_size_covers_bf16(L):
+    """At 4 bits up to 8 rows an odd N (or an X too large for shared memory) goes to the tensor-core
+    path with bf16 activations, as at 3 bits: the size is the same for both."""
+    for M, N, K in ((1, 1000, 11008), (4, 1000, 11008), (8, 40, 4096), (8, 4096, 65536)):
+        need = L.awq_gemm_workspace_size(M, N, K, 4)
+        assert need == L.awq_gemm_workspace_size(M, N, K, 3) and need >= 2 * M * N * 4
+    assert L.awq_gemm_workspace_size(8, 1008, 4096, 4) == 0

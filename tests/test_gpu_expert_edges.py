@@ -204,3 +204,15 @@ def test_silu_mul_of_many_rows_an_expert(awq, counts, I, K):  # noqa: F811
         assert_within(got, want, tol, e)
         # as a whole: fp16's rounding, and what fp32 sums of K / 16 steps add to it
         assert np.linalg.norm(f64(got) - want) <= 1.05 * 2.0 ** -11 * 3 ** -0.5 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1000, 11008), (4, 1001, 4096), (8, 40, 4096)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_plain_product_of_few_rows_and_an_odd_width(awq, M, N, K, dtype):  # noqa: F811
+    rng = np.random.default_rng([M, N, K])
+    layer = Layer(rng, 1, N, K, 4, dtype)
+    X = tokens(rng, M, K, dtype)
+    y = awq.awq_gemm_w4a16(X, layer.qw[0], layer.sc[0], layer.z[0], N, K, 4)
+    awq.awq_check_error()
+    want, tol = layer.want(0, X)
+    assert assert_within(y, want, tol) <= 3 * U[dtype]

@@ -753,9 +753,11 @@ awq_status awq_silu_mul_gemm(const awq_f16* X, int64_t M, const awq_f16* W_gate,
 // ------------------------------------------------------------------ GEMM
 size_t awq_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int bits) {
   if (M <= 0 || K <= 0 || N <= 0) return 0;
-  // the decode kernels need none; a call the streaming kernel cannot take (8 < M <= 16 with
-  // an X too large for it, or 3 bits with N % 16 != 0) takes the tensor-core path below
-  if (M <= 16 && (gemv_stream_fits(M, N, K) || (bits == 4 && M <= 8))) return 0;
+  // the streaming kernel needs none; a call that it cannot take (an X too large for it, or
+  // N % 16 != 0) may take the tensor-core path below: with bf16 activations, at 3 bits or past 8
+  // rows (the size covers either type)
+  (void)bits;
+  if (M <= 16 && gemv_stream_fits(M, N, K)) return 0;
   const int splits = splitk_for(M, N, K);
   return splits > 1 ? align256(static_cast<size_t>(splits) * M * N * sizeof(float)) : 0;
 }
