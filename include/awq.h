@@ -208,7 +208,10 @@ AWQ_API awq_status awq_silu_mul_gemm(const awq_f16* X, int64_t M, const awq_f16*
  * so no extra pass over X is made.
  * M <= 16 runs a decode kernel (HBM-bound GEMV, 4 or 3 bits; when N is a multiple of 16 and
  * X fits in one CTA's shared memory, or, for fp16 4-bit M <= 8, a register-streaming kernel);
- * other calls run the tensor-core kernel.
+ * other calls run the tensor-core kernel. (One fp16 row at 4 bits: the decode kernel divides half
+ * of the columns by 16 in fp16, so values below 2^-10 may lose their last bits there: a row of
+ * magnitude 1e-4 is off by 5.5e-4 of the output's norm instead of 2.1e-4. The call with a fused
+ * epilogue, with no part, does not.)
  * X: fp16 [M, K]; Y: fp16 [M, N]. M = 0 or N = 0 is a no-op.
  * flags: 0, or AWQ_GEMM_WEIGHTS_READY. The kernels are launched with programmatic dependent
  * launch, so a kernel of this call may start while the kernel launched just before it on
